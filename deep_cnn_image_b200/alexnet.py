@@ -16,6 +16,8 @@ LIB_PATH = os.path.join(_HERE, "libalexnet.so")
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_TIMEOUT, ERR_LABEL_RANGE = range(6)
 FP32, BF16 = 0, 1
+E4M3, E5M2 = 0, 1
+SILU, GELU, RELU = 0, 1, 2
 TRAIN, INFERENCE = 0, 1
 STATUS_NAMES = {0: "OK", 1: "INVALID_ARG", 2: "UNSUPPORTED", 3: "CUDA", 4: "TIMEOUT",
                 5: "LABEL_RANGE"}
@@ -96,6 +98,20 @@ def _load():
         "alexnet_op_dropout_mask": (st, [c_uint64, c_uint32, c_uint32, c_float, i, i, vp, vp, sz,
                                          vp]),
         "alexnet_op_philox": (st, [vp, vp, i, vp, vp]),
+        "alexnet_f8_scale_bytes": (sz, [c_int64, i]),
+        "alexnet_op_f8_quant": (st, [vp, c_int64, i, i, vp, vp, vp]),
+        "alexnet_op_f8_dequant": (st, [vp, vp, c_int64, i, i, vp, vp]),
+        "alexnet_op_rmsnorm_fwd": (st, [vp, vp, vp, c_int64, i, c_float, vp, vp, vp, vp, vp, vp]),
+        "alexnet_rmsnorm_workspace_bytes": (sz, [c_int64, i]),
+        "alexnet_op_rmsnorm_bwd": (st, [vp, vp, vp, vp, vp, c_int64, i, vp, vp, vp, sz, vp]),
+        "alexnet_fc_f8_workspace_bytes": (sz, [i, i, i]),
+        "alexnet_op_fc_f8_fwd": (st, [vp, vp, i, i, i, vp, vp, i, i, i, vp, vp, sz, vp]),
+        "alexnet_gated_workspace_bytes": (sz, [i, i, i]),
+        "alexnet_op_gated_fwd": (st, [vp, i, i, vp, i, i, vp, i, vp, vp, sz, vp]),
+        "alexnet_op_gated_bwd": (st, [vp, vp, i, vp, i, i, vp, i, i, vp, vp, vp, sz, vp]),
+        "alexnet_op_gated_fwd_ckpt8": (st, [vp, i, i, vp, i, i, vp, vp, vp, vp, sz, vp]),
+        "alexnet_op_gated_bwd_ckpt8": (st, [vp, vp, vp, vp, vp, i, i, vp, i, i, vp, vp, vp, sz,
+                                            vp]),
         "alexnet_op_wait_probe": (st, [vp, c_int64, vp]),
         "alexnet_debug_copy": (st, [vp, i, vp, sz, vp]),
         "alexnet_debug_keep": (st, [vp, i]),
@@ -381,6 +397,72 @@ def op_pool_lrn_bwd(dy, argmax, a, B, H, W, C, z, k, alpha, beta, dl, da, stream
 def op_softmax_ce(logits, labels, B, N, probs, dlogits, loss, ws, stream=None):
     return _op("alexnet_op_softmax_ce", _ptr(logits), _ptr(labels), B, N, _ptr(probs),
                _ptr(dlogits), _ptr(loss), _ptr(ws), ws.numel(), _stream(stream))
+
+
+def f8_scale_bytes(rows, cols):
+    return lib.alexnet_f8_scale_bytes(rows, cols)
+
+
+def op_f8_quant(x, rows, cols, fmt, q, scales, stream=None):
+    """bf16 rows -> 8-bit codes (uint8) and scales (uint8, f8_scale_bytes)."""
+    return _op("alexnet_op_f8_quant", _ptr(x), rows, cols, fmt, _ptr(q), _ptr(scales),
+               _stream(stream))
+
+
+def op_f8_dequant(q, scales, rows, cols, fmt, x, stream=None):
+    return _op("alexnet_op_f8_dequant", _ptr(q), _ptr(scales), rows, cols, fmt, _ptr(x),
+               _stream(stream))
+
+
+def op_rmsnorm_fwd(x, res, gamma, rows, cols, eps, sum, y, rstd, q, scales, stream=None):
+    """Norm of x + res; sum, y, rstd and the pair q, scales may be None."""
+    return _op("alexnet_op_rmsnorm_fwd", _ptr(x), _ptr(res), _ptr(gamma), rows, cols, eps,
+               _ptr(sum), _ptr(y), _ptr(rstd), _ptr(q), _ptr(scales), _stream(stream))
+
+
+def rmsnorm_workspace_bytes(rows, cols):
+    return lib.alexnet_rmsnorm_workspace_bytes(rows, cols)
+
+
+def op_rmsnorm_bwd(dy, dsum, s, gamma, rstd, rows, cols, dx, dgamma, ws, stream=None):
+    return _op("alexnet_op_rmsnorm_bwd", _ptr(dy), _ptr(dsum), _ptr(s), _ptr(gamma), _ptr(rstd),
+               rows, cols, _ptr(dx), _ptr(dgamma), _ptr(ws), ws.numel(), _stream(stream))
+
+
+def fc_f8_workspace_bytes(B, In, Out):
+    return lib.alexnet_fc_f8_workspace_bytes(B, In, Out)
+
+
+def op_fc_f8_fwd(x, xs, x_fmt, B, In, w, wscales, w_fmt, Out, y_dtype, y, ws, stream=None):
+    return _op("alexnet_op_fc_f8_fwd", _ptr(x), _ptr(xs), x_fmt, B, In, _ptr(w), _ptr(wscales),
+               w_fmt, Out, y_dtype, _ptr(y), _ptr(ws), ws.numel(), _stream(stream))
+
+
+def gated_workspace_bytes(B, In, F):
+    return lib.alexnet_gated_workspace_bytes(B, In, F)
+
+
+def op_gated_fwd(x, B, In, w, F, act, h, gu_dtype, gu, ws, stream=None):
+    """h = act(x wg^T) * (x wu^T), w = [wg; wu]; gu (None: not kept) in FP32 or
+    BF16 for the backward."""
+    return _op("alexnet_op_gated_fwd", _ptr(x), B, In, _ptr(w), F, act, _ptr(h), gu_dtype,
+               _ptr(gu), _ptr(ws), ws.numel(), _stream(stream))
+
+
+def op_gated_bwd(dh, x, gu_dtype, gu, B, In, w, F, act, dx, dw, ws, stream=None):
+    return _op("alexnet_op_gated_bwd", _ptr(dh), _ptr(x), gu_dtype, _ptr(gu), B, In, _ptr(w), F,
+               act, _ptr(dx), _ptr(dw), _ptr(ws), ws.numel(), _stream(stream))
+
+
+def op_gated_fwd_ckpt8(x, B, In, w, F, act, h, guq, gus, ws, stream=None):
+    """op_gated_fwd keeping g and u in 8 bits for op_gated_bwd_ckpt8."""
+    return _op("alexnet_op_gated_fwd_ckpt8", _ptr(x), B, In, _ptr(w), F, act, _ptr(h), _ptr(guq),
+               _ptr(gus), _ptr(ws), ws.numel(), _stream(stream))
+
+
+def op_gated_bwd_ckpt8(dh, xq, xs, guq, gus, B, In, w, F, act, dx, dw, ws, stream=None):
+    return _op("alexnet_op_gated_bwd_ckpt8", _ptr(dh), _ptr(xq), _ptr(xs), _ptr(guq), _ptr(gus),
+               B, In, _ptr(w), F, act, _ptr(dx), _ptr(dw), _ptr(ws), ws.numel(), _stream(stream))
 
 
 def ensemble_workspace_bytes(n_models, B):

@@ -1,0 +1,75 @@
+// f8.cuh -- the 8-bit row format of the feed-forward operators: codes in
+// e4m3 or e5m2 with one power-of-two scale per row and 128 columns, and the
+// place of a scale byte in its tile (alexnet_ops.h, "8-bit rows").
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <cstdint>
+
+namespace alx {
+
+constexpr int F8_BLOCK = 128;         // columns that share a scale
+constexpr int F8_TILE_ROWS = 128;     // rows and
+constexpr int F8_TILE_COLS = 512;     // columns of one tile of scales,
+constexpr int F8_TILE_BYTES = 512;    // one byte per row and block
+
+// Byte offset of the scale of (row, block) in a matrix of `col_tiles` =
+// ceil(cols / 512) scale tiles per 128 rows.
+__host__ __device__ __forceinline__ size_t f8_scale_at(int64_t row, int block, int col_tiles) {
+  const size_t tile = static_cast<size_t>(row >> 7) * col_tiles + (block >> 2);
+  const int r = static_cast<int>(row & 127);
+  return tile * F8_TILE_BYTES + (r & 31) * 16 + (r >> 5) * 4 + (block & 3);
+}
+
+// The scale byte e + 127 of a block whose largest magnitude is amax (finite,
+// >= 0): the smallest e with amax <= fmax * 2^e, fmax = 1.75 * 2^8 (e4m3) or
+// 1.75 * 2^15 (e5m2).  With amax = m * 2^k (1 <= m < 2) that is k - 8 (15),
+// plus one for m > 1.75: adding 2^21 - 1 to the bits carries into the
+// exponent exactly then.  Below 2^-127 the byte stays 0 (the codes
+// underflow).
+__device__ __forceinline__ uint32_t f8_scale_byte(float amax, int e5m2) {
+  const int e = static_cast<int>((__float_as_uint(amax) + 0x1FFFFFu) >> 23) - (e5m2 ? 15 : 8);
+  return e < 0 ? 0u : static_cast<uint32_t>(e);
+}
+// 2^-e (what values are multiplied with) and 2^e (what codes are) of a byte
+__device__ __forceinline__ float f8_scale_inv(uint32_t byte) {
+  return __uint_as_float((254u - byte) << 23);
+}
+__device__ __forceinline__ float f8_scale_val(uint32_t byte) {
+  return __uint_as_float(byte ? byte << 23 : 0x00400000u);
+}
+
+// NaN for infinities and NaN, the value itself (a zero's sign included)
+// otherwise: what a code can hold (e4m3 has no infinity), and what fmaxf
+// leaves out of a maximum.
+__device__ __forceinline__ float f8_finite(float v) {
+  return fabsf(v) <= 3.402823466e38f ? v : __uint_as_float(0x7FFFFFFFu);
+}
+
+// Two values -> two codes (low byte first), four values -> one word.
+__device__ __forceinline__ uint32_t f8_pack2(float a, float b, int e5m2) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE,
+                                  e5m2 ? __NV_E5M2 : __NV_E4M3);
+}
+__device__ __forceinline__ uint32_t f8_pack4(float a, float b, float c, float d, int e5m2) {
+  return f8_pack2(a, b, e5m2) | (f8_pack2(c, d, e5m2) << 16);
+}
+// Four codes -> four values (before the scale).
+__device__ __forceinline__ void f8_unpack4(uint32_t w, int e5m2, float (&v)[4]) {
+  const __nv_fp8_interpretation_t t = e5m2 ? __NV_E5M2 : __NV_E4M3;
+  const __half2 lo = __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w), t));
+  const __half2 hi =
+      __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> 16), t));
+  const float2 a = __half22float2(lo), b = __half22float2(hi);
+  v[0] = a.x;
+  v[1] = a.y;
+  v[2] = b.x;
+  v[3] = b.y;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+
+}  // namespace alx

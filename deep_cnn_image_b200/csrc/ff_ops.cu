@@ -1,0 +1,245 @@
+// ff_ops.cu -- entry points of the feed-forward operators (alexnet_ops.h):
+// argument checks, workspace layout and launches.
+#include <cstring>
+
+#include "alexnet.h"
+#include "alexnet_ops.h"
+#include "f8.cuh"
+#include "ff.h"
+#include "gemm.h"
+
+using namespace alx;
+
+namespace {
+
+constexpr int MAX_DIM = 1 << 24;  // columns of any matrix here: keeps 2F and tile counts in an int
+
+size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+alexnet_status done(cudaError_t e) { return e == cudaSuccess ? ALEXNET_OK : ALEXNET_ERR_CUDA; }
+bool bad16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; }
+template <typename... P>
+bool bad16(const void* p, P... more) {
+  return bad16(p) || bad16(more...);
+}
+bool bad_dtype(int d) { return d != ALEXNET_FP32 && d != ALEXNET_BF16; }
+bool bad_fmt(int f) { return f != ALEXNET_E4M3 && f != ALEXNET_E5M2; }
+cudaStream_t cu(void* s) { return static_cast<cudaStream_t>(s); }
+const bf16* B16(const void* p) { return static_cast<const bf16*>(p); }
+bf16* B16(void* p) { return static_cast<bf16*>(p); }
+uint8_t* U8(void* p) { return static_cast<uint8_t*>(p); }
+const uint8_t* U8(const void* p) { return static_cast<const uint8_t*>(p); }
+
+bool gated_dims(int B, int In, int F, int step) {
+  return B >= 1 && In >= 1 && F >= 1 && In % step == 0 && F % step == 0;
+}
+
+// D[M, N] = A[M, K] B[N, K]^T on the library's GEMM kernel
+alexnet_status gemm(const void* a, int amn, const void* b, int bmn, int M, int N, int K, int epi,
+                    void* out, int* status, cudaStream_t s) {
+  GemmDesc d;
+  memset(&d, 0, sizeof(d));
+  d.asrc = amn ? A_TMA_MN : A_TMA_K;
+  d.bsrc = bmn ? B_TMA_MN : B_TMA_K;
+  d.bn = 256;
+  d.args.M = M;
+  d.args.N = N;
+  d.args.Kblocks = (K + 63) / 64;
+  d.args.kb_per_split = d.args.Kblocks;
+  d.args.groups = 1;
+  d.args.epi = epi;
+  d.args.out = out;
+  d.args.ld_out = N;
+  d.args.status = status;
+  const bool ok =
+      (amn ? make_tmap_bf16(&d.tmA, a, M, K, 2ull * M, 64, 64)
+           : make_tmap_bf16(&d.tmA, a, K, M, 2ull * K, 64, 128)) &&
+      (bmn ? make_tmap_bf16(&d.tmB, b, N, K, 2ull * N, 64, 64)
+           : make_tmap_bf16(&d.tmB, b, K, N, 2ull * K, 64, 256));
+  if (!ok) return ALEXNET_ERR_INVALID_ARG;
+  if (!gemm_finalize(&d, ff_num_sms())) return ALEXNET_ERR_UNSUPPORTED;
+  return done(gemm_launch(d, s));
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t alexnet_f8_scale_bytes(int64_t rows, int cols) {
+  if (rows < 1 || cols < 1 || cols % 16) return 0;
+  return static_cast<size_t>((rows + F8_TILE_ROWS - 1) / F8_TILE_ROWS) *
+         ((cols + F8_TILE_COLS - 1) / F8_TILE_COLS) * F8_TILE_BYTES;
+}
+
+alexnet_status alexnet_op_f8_quant(const void* x, int64_t rows, int cols, int fmt, void* q,
+                                   uint8_t* scales, void* stream) {
+  if (!x || !q || !scales || rows < 1 || cols < 1 || cols % 16 || bad_fmt(fmt) ||
+      bad16(x, q, scales))
+    return ALEXNET_ERR_INVALID_ARG;
+  return done(launch_f8_quant(B16(x), rows, cols, fmt, U8(q), scales, cu(stream)));
+}
+
+alexnet_status alexnet_op_f8_dequant(const void* q, const uint8_t* scales, int64_t rows, int cols,
+                                     int fmt, void* x, void* stream) {
+  if (!x || !q || !scales || rows < 1 || cols < 1 || cols % 16 || bad_fmt(fmt) ||
+      bad16(x, q, scales))
+    return ALEXNET_ERR_INVALID_ARG;
+  return done(launch_f8_dequant(U8(q), scales, rows, cols, fmt, B16(x), cu(stream)));
+}
+
+alexnet_status alexnet_op_rmsnorm_fwd(const void* x, const void* res, const float* gamma,
+                                      int64_t rows, int cols, float eps, void* sum, void* y,
+                                      float* rstd, void* q, uint8_t* scales, void* stream) {
+  if (!x || !gamma || rows < 1 || cols < 1 || cols % 8 || (q && cols % 16) || !q != !scales ||
+      !(eps > 0.f) || bad16(x, res, gamma, sum, y, rstd, q, scales))
+    return ALEXNET_ERR_INVALID_ARG;
+  if (cols > RMSNORM_MAX_COLS || rows > 0x7FFFFFFF) return ALEXNET_ERR_UNSUPPORTED;
+  return done(launch_rmsnorm_fwd(B16(x), B16(res), gamma, rows, cols, eps, B16(sum), B16(y), rstd,
+                                 U8(q), scales, cu(stream)));
+}
+
+size_t alexnet_rmsnorm_workspace_bytes(int64_t rows, int cols) {
+  if (rows < 1 || cols < 1 || cols % 8 || cols > RMSNORM_MAX_COLS || rows > 0x7FFFFFFF) return 0;
+  return 256 + static_cast<size_t>(rmsnorm_bwd_parts(rows, cols)) * cols * 4;
+}
+
+alexnet_status alexnet_op_rmsnorm_bwd(const void* dy, const void* dsum, const void* s,
+                                      const float* gamma, const float* rstd, int64_t rows,
+                                      int cols, void* dx, float* dgamma, void* ws, size_t ws_bytes,
+                                      void* stream) {
+  if (!dy || !s || !gamma || !rstd || !dx || rows < 1 || cols < 1 || cols % 8 ||
+      bad16(dy, dsum, s, gamma, rstd, dx, dgamma, ws))
+    return ALEXNET_ERR_INVALID_ARG;
+  if (cols > RMSNORM_MAX_COLS || rows > 0x7FFFFFFF) return ALEXNET_ERR_UNSUPPORTED;
+  if (!ws || ws_bytes < alexnet_rmsnorm_workspace_bytes(rows, cols)) return ALEXNET_ERR_INVALID_ARG;
+  return done(launch_rmsnorm_bwd(B16(dy), B16(dsum), B16(s), gamma, rstd, rows, cols, B16(dx),
+                                 dgamma, reinterpret_cast<float*>(U8(ws) + 256), cu(stream)));
+}
+
+size_t alexnet_fc_f8_workspace_bytes(int B, int In, int Out) {
+  if (B < 1 || In < 1 || Out < 1 || In % 16 || Out % 8 || In > MAX_DIM || Out > MAX_DIM) return 0;
+  return 256 + up256(2ull * B * In) + up256(2ull * Out * In);
+}
+
+alexnet_status alexnet_op_fc_f8_fwd(const void* x, const uint8_t* xs, int x_fmt, int B, int In,
+                                    const void* w, const uint8_t* wscales, int w_fmt, int Out,
+                                    int y_dtype, void* y, void* ws, size_t ws_bytes,
+                                    void* stream) {
+  if (!x || !xs || !w || !wscales || !y || B < 1 || In < 1 || Out < 1 || In % 16 || Out % 8 ||
+      bad_fmt(x_fmt) || bad_fmt(w_fmt) || bad_dtype(y_dtype) ||
+      bad16(x, xs, w, wscales, y, ws))
+    return ALEXNET_ERR_INVALID_ARG;
+  if (In > MAX_DIM || Out > MAX_DIM) return ALEXNET_ERR_UNSUPPORTED;
+  if (!ws || ws_bytes < alexnet_fc_f8_workspace_bytes(B, In, Out)) return ALEXNET_ERR_INVALID_ARG;
+  uint8_t* p = U8(ws) + 256;
+  bf16* xb = reinterpret_cast<bf16*>(p);
+  bf16* wb = reinterpret_cast<bf16*>(p + up256(2ull * B * In));
+  cudaStream_t s = cu(stream);
+  cudaMemsetAsync(ws, 0, 4, s);
+  if (cudaError_t e = launch_f8_dequant(U8(x), xs, B, In, x_fmt, xb, s)) return done(e);
+  if (cudaError_t e = launch_f8_dequant(U8(w), wscales, Out, In, w_fmt, wb, s)) return done(e);
+  return gemm(xb, 0, wb, 0, B, Out, In, y_dtype == ALEXNET_FP32 ? EPI_F32 : EPI_BF16, y,
+              static_cast<int*>(ws), s);
+}
+
+size_t alexnet_gated_workspace_bytes(int B, int In, int F) {
+  if (!gated_dims(B, In, F, 8) || In > MAX_DIM || F > MAX_DIM) return 0;
+  return 256 + up256(8ull * B * F) + up256(2ull * B * In);
+}
+
+}  // extern "C"
+
+namespace {
+
+bool bad_act(int a) { return a < ALEXNET_SILU || a > ALEXNET_RELU; }
+
+GateSave save_of(int dtype, const void* gu) {
+  GateSave v{};
+  if (dtype == ALEXNET_FP32)
+    v.f32 = static_cast<float*>(const_cast<void*>(gu));
+  else
+    v.b16 = B16(const_cast<void*>(gu));
+  return v;
+}
+GateSave save_of(const void* guq, const uint8_t* gus) {
+  GateSave v{};
+  v.q = U8(const_cast<void*>(guq));
+  v.qs = const_cast<uint8_t*>(gus);
+  return v;
+}
+
+alexnet_status gated_fwd(const void* x, int B, int In, const void* w, int F, int act, void* h,
+                         const GateSave& save, void* ws, cudaStream_t s) {
+  float* z = reinterpret_cast<float*>(U8(ws) + 256);
+  cudaMemsetAsync(ws, 0, 4, s);
+  if (alexnet_status e = gemm(x, 0, w, 0, B, 2 * F, In, EPI_F32, z, static_cast<int*>(ws), s))
+    return e;
+  return done(launch_gate_fwd(z, B, F, act, B16(h), save, s));
+}
+
+alexnet_status gated_bwd(const void* dh, const void* x, const GateSave& save, int B, int In,
+                         const void* w, int F, int act, void* dx, void* dw, void* ws,
+                         cudaStream_t s) {
+  bf16* dz = reinterpret_cast<bf16*>(U8(ws) + 256);
+  cudaMemsetAsync(ws, 0, 4, s);
+  if (cudaError_t e = launch_gate_bwd(B16(dh), save, B, F, act, dz, s)) return done(e);
+  if (dx)
+    if (alexnet_status e =
+            gemm(dz, 0, w, 1, B, In, 2 * F, EPI_BF16, dx, static_cast<int*>(ws), s))
+      return e;
+  return dw ? gemm(dz, 1, x, 1, 2 * F, In, B, EPI_BF16, dw, static_cast<int*>(ws), s) : ALEXNET_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+alexnet_status alexnet_op_gated_fwd(const void* x, int B, int In, const void* w, int F, int act,
+                                    void* h, int gu_dtype, void* gu, void* ws, size_t ws_bytes,
+                                    void* stream) {
+  if (!x || !w || !h || !gated_dims(B, In, F, 8) || bad_act(act) || bad_dtype(gu_dtype) ||
+      bad16(x, w, h, gu, ws))
+    return ALEXNET_ERR_INVALID_ARG;
+  if (In > MAX_DIM || F > MAX_DIM) return ALEXNET_ERR_UNSUPPORTED;
+  if (!ws || ws_bytes < alexnet_gated_workspace_bytes(B, In, F)) return ALEXNET_ERR_INVALID_ARG;
+  return gated_fwd(x, B, In, w, F, act, h, save_of(gu_dtype, gu), ws, cu(stream));
+}
+
+alexnet_status alexnet_op_gated_fwd_ckpt8(const void* x, int B, int In, const void* w, int F,
+                                          int act, void* h, void* guq, uint8_t* gus, void* ws,
+                                          size_t ws_bytes, void* stream) {
+  if (!x || !w || !h || !guq || !gus || !gated_dims(B, In, F, 16) || bad_act(act) ||
+      bad16(x, w, h, guq, gus, ws))
+    return ALEXNET_ERR_INVALID_ARG;
+  if (In > MAX_DIM || F > MAX_DIM) return ALEXNET_ERR_UNSUPPORTED;
+  if (!ws || ws_bytes < alexnet_gated_workspace_bytes(B, In, F)) return ALEXNET_ERR_INVALID_ARG;
+  return gated_fwd(x, B, In, w, F, act, h, save_of(guq, gus), ws, cu(stream));
+}
+
+alexnet_status alexnet_op_gated_bwd(const void* dh, const void* x, int gu_dtype, const void* gu,
+                                    int B, int In, const void* w, int F, int act, void* dx,
+                                    void* dw, void* ws, size_t ws_bytes, void* stream) {
+  if (!dh || !x || !gu || !w || !gated_dims(B, In, F, 8) || bad_act(act) || bad_dtype(gu_dtype) ||
+      bad16(dh, x, gu, w, dx, dw, ws))
+    return ALEXNET_ERR_INVALID_ARG;
+  if (In > MAX_DIM || F > MAX_DIM) return ALEXNET_ERR_UNSUPPORTED;
+  if (!ws || ws_bytes < alexnet_gated_workspace_bytes(B, In, F)) return ALEXNET_ERR_INVALID_ARG;
+  return gated_bwd(dh, x, save_of(gu_dtype, gu), B, In, w, F, act, dx, dw, ws, cu(stream));
+}
+
+alexnet_status alexnet_op_gated_bwd_ckpt8(const void* dh, const void* xq, const uint8_t* xs,
+                                          const void* guq, const uint8_t* gus, int B, int In,
+                                          const void* w, int F, int act, void* dx, void* dw,
+                                          void* ws, size_t ws_bytes, void* stream) {
+  if (!dh || !xq || !xs || !guq || !gus || !w || !gated_dims(B, In, F, 16) || bad_act(act) ||
+      bad16(dh, xq, xs, guq, gus, w, dx, dw, ws))
+    return ALEXNET_ERR_INVALID_ARG;
+  if (In > MAX_DIM || F > MAX_DIM) return ALEXNET_ERR_UNSUPPORTED;
+  if (!ws || ws_bytes < alexnet_gated_workspace_bytes(B, In, F)) return ALEXNET_ERR_INVALID_ARG;
+  bf16* xb = reinterpret_cast<bf16*>(U8(ws) + 256 + up256(8ull * B * F));
+  if (dw)
+    if (cudaError_t e = launch_f8_dequant(U8(xq), xs, B, In, ALEXNET_E4M3, xb, cu(stream)))
+      return done(e);
+  return gated_bwd(dh, xb, save_of(guq, gus), B, In, w, F, act, dx, dw, ws, cu(stream));
+}
+
+}  // extern "C"

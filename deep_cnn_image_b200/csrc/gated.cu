@@ -1,0 +1,171 @@
+// gated.cu -- the gated block's elementwise parts: gate and product of the
+// projections, and the gradients of both.
+#include <cuda_bf16.h>
+
+#include "f8.cuh"
+#include "ff.h"
+#include "gate.cuh"
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace alx {
+
+namespace {
+
+// 16 lanes per 128-column block of a row, 8 columns of g and u each: h =
+// a(g) u, and the projections themselves in bf16 or as 8-bit rows.
+__global__ void __launch_bounds__(256)
+    k_gate_fwd(const float* __restrict__ z, int B, int F, int act, bf16* __restrict__ h,
+               const GateSave save) {
+  bf16* gu = save.b16;
+  uint8_t *guq = save.q, *gus = save.qs;
+  const int blocks = (F + F8_BLOCK - 1) / F8_BLOCK;
+  const int col_tiles = (F + F8_TILE_COLS - 1) / F8_TILE_COLS;
+  const size_t half_s = static_cast<size_t>((B + 127) / 128) * col_tiles * F8_TILE_BYTES;
+  const int64_t total = static_cast<int64_t>(B) * blocks;
+  const int sub = threadIdx.x & 15;
+  const uint32_t mask = 0xFFFFu << (threadIdx.x & 16);
+  for (int64_t b = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 4); b < total;
+       b += static_cast<int64_t>(gridDim.x) * 16) {
+    const int64_t row = b / blocks;
+    const int blk = static_cast<int>(b - row * blocks);
+    const int col = blk * F8_BLOCK + sub * 8;
+    float p[2][8] = {};
+    if (col < F) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float* src = z + row * 2 * F + k * static_cast<int64_t>(F) + col;
+        const float4 a = *reinterpret_cast<const float4*>(src);
+        const float4 c = *reinterpret_cast<const float4*>(src + 4);
+        p[k][0] = a.x, p[k][1] = a.y, p[k][2] = a.z, p[k][3] = a.w;
+        p[k][4] = c.x, p[k][5] = c.y, p[k][6] = c.z, p[k][7] = c.w;
+      }
+      uint32_t o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        o[i] = pack_bf16(gate_value(p[0][2 * i], act) * p[1][2 * i],
+                         gate_value(p[0][2 * i + 1], act) * p[1][2 * i + 1]);
+      *reinterpret_cast<uint4*>(h + row * F + col) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (save.f32 && col < F) {
+        float4* o = reinterpret_cast<float4*>(save.f32 + row * 2 * F + k * static_cast<int64_t>(F) + col);
+        o[0] = make_float4(p[k][0], p[k][1], p[k][2], p[k][3]);
+        o[1] = make_float4(p[k][4], p[k][5], p[k][6], p[k][7]);
+      }
+      if (gu && col < F)
+        *reinterpret_cast<uint4*>(gu + row * 2 * F + k * static_cast<int64_t>(F) + col) =
+            make_uint4(pack_bf16(p[k][0], p[k][1]), pack_bf16(p[k][2], p[k][3]),
+                       pack_bf16(p[k][4], p[k][5]), pack_bf16(p[k][6], p[k][7]));
+      if (guq) {
+        float a = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          p[k][i] = f8_finite(p[k][i]);
+          a = fmaxf(a, fabsf(p[k][i]));
+        }
+#pragma unroll
+        for (int o = 8; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(mask, a, o));
+        const uint32_t s = f8_scale_byte(a, 0);
+        const float inv = f8_scale_inv(s);
+        if (col < F)
+          *reinterpret_cast<uint2*>(guq + (k * static_cast<int64_t>(B) + row) * F + col) =
+              make_uint2(f8_pack4(p[k][0] * inv, p[k][1] * inv, p[k][2] * inv, p[k][3] * inv, 0),
+                         f8_pack4(p[k][4] * inv, p[k][5] * inv, p[k][6] * inv, p[k][7] * inv, 0));
+        if (sub == 0)
+          gus[k * half_s + f8_scale_at(row, blk, col_tiles)] = static_cast<uint8_t>(s);
+      }
+    }
+  }
+}
+
+// dg = dh u a'(g), du = dh a(g); 8 columns per thread, the projections from
+// bf16 (KIND 0), 8-bit rows (1) or fp32 (2).  Bound by its bytes: 6, 4 or 10
+// read and 4 written per element of h.
+template <int KIND>
+__global__ void __launch_bounds__(256)
+    k_gate_bwd(const bf16* __restrict__ dh, const GateSave save, int B, int F, int act,
+               bf16* __restrict__ dz) {
+  const bf16* __restrict__ gu = save.b16;
+  const uint8_t *__restrict__ guq = save.q, *__restrict__ gus = save.qs;
+  const int vecs = F >> 3;
+  const int col_tiles = (F + F8_TILE_COLS - 1) / F8_TILE_COLS;
+  const size_t half_s = static_cast<size_t>((B + 127) / 128) * col_tiles * F8_TILE_BYTES;
+  const int64_t total = static_cast<int64_t>(B) * vecs;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total;
+       i += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t row = i / vecs;
+    const int col = static_cast<int>(i - row * vecs) * 8;
+    float d[8], p[2][8];
+    unpack8_bits(*reinterpret_cast<const uint4*>(dh + i * 8), d);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (KIND == 1) {
+        const uint2 w =
+            *reinterpret_cast<const uint2*>(guq + (k * static_cast<int64_t>(B) + row) * F + col);
+        const float sc = f8_scale_val(gus[k * half_s + f8_scale_at(row, col >> 7, col_tiles)]);
+        float a[4], b[4];
+        f8_unpack4(w.x, 0, a);
+        f8_unpack4(w.y, 0, b);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          p[k][j] = a[j] * sc;
+          p[k][4 + j] = b[j] * sc;
+        }
+      } else if (KIND == 2) {
+        const float4* src = reinterpret_cast<const float4*>(save.f32 + row * 2 * F +
+                                                            k * static_cast<int64_t>(F) + col);
+        const float4 a = src[0], c = src[1];
+        p[k][0] = a.x, p[k][1] = a.y, p[k][2] = a.z, p[k][3] = a.w;
+        p[k][4] = c.x, p[k][5] = c.y, p[k][6] = c.z, p[k][7] = c.w;
+      } else {
+        unpack8_bits(*reinterpret_cast<const uint4*>(gu + row * 2 * F +
+                                                     k * static_cast<int64_t>(F) + col),
+                     p[k]);
+      }
+    }
+    uint32_t og[4], ou[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float a0, e0, a1, e1;
+      gate_both(p[0][2 * j], act, a0, e0);
+      gate_both(p[0][2 * j + 1], act, a1, e1);
+      og[j] = pack_bf16(d[2 * j] * p[1][2 * j] * e0, d[2 * j + 1] * p[1][2 * j + 1] * e1);
+      ou[j] = pack_bf16(d[2 * j] * a0, d[2 * j + 1] * a1);
+    }
+    bf16* o = dz + row * 2 * F + col;
+    *reinterpret_cast<uint4*>(o) = make_uint4(og[0], og[1], og[2], og[3]);
+    *reinterpret_cast<uint4*>(o + F) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
+  }
+}
+
+int grid_for(int64_t blocks) {
+  const int64_t most = static_cast<int64_t>(ff_num_sms()) * 16;
+  return static_cast<int>(blocks < most ? blocks : most);
+}
+
+}  // namespace
+
+cudaError_t launch_gate_fwd(const float* z, int B, int F, int act, bf16* h, const GateSave& save,
+                            cudaStream_t s) {
+  const int64_t blocks = static_cast<int64_t>(B) * ((F + F8_BLOCK - 1) / F8_BLOCK);
+  k_gate_fwd<<<grid_for((blocks + 15) / 16), 256, 0, s>>>(z, B, F, act, h, save);
+  count_launch();
+  return cudaGetLastError();
+}
+
+cudaError_t launch_gate_bwd(const bf16* dh, const GateSave& save, int B, int F, int act, bf16* dz,
+                            cudaStream_t s) {
+  const int grid = grid_for((static_cast<int64_t>(B) * (F >> 3) + 255) / 256);
+  if (save.b16)
+    k_gate_bwd<0><<<grid, 256, 0, s>>>(dh, save, B, F, act, dz);
+  else if (save.q)
+    k_gate_bwd<1><<<grid, 256, 0, s>>>(dh, save, B, F, act, dz);
+  else
+    k_gate_bwd<2><<<grid, 256, 0, s>>>(dh, save, B, F, act, dz);
+  count_launch();
+  return cudaGetLastError();
+}
+
+}  // namespace alx

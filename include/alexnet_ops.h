@@ -163,6 +163,127 @@ ALEXNET_API alexnet_status alexnet_op_dropout_mask(uint64_t seed, uint32_t layer
 ALEXNET_API alexnet_status alexnet_op_philox(const uint32_t* ctr, const uint32_t* key, int n, uint32_t* out,
                                  void* stream);
 
+/* ------------------------------------------------------------------------
+ * Feed-forward operators: a normalised, gated fully-connected block in bf16
+ * and 8 bits, next to the FC products and the normalisation above.  The
+ * pages have no counterpart.
+ *
+ * 8-bit rows.  A matrix [rows, cols] (cols % 16 == 0) is held as one code
+ * per value, row-major, and one scale per row and block of 128 columns (the
+ * last block of a row may be shorter).  A block's scale is 2^e with the
+ * smallest integer e, -127 <= e <= 127, for which its largest magnitude is
+ * at most the type's largest value (E4M3 448, E5M2 57344) times 2^e (e =
+ * -127 for a block of zeros); a code is value * 2^-e rounded to nearest
+ * even.  A NaN keeps its place as NaN, an infinity becomes NaN, and neither
+ * counts for e.  The scales are bytes e + 127 in the order in which the
+ * tensor cores take them: tiles of 128 rows x 4 blocks of 512 bytes, tiles of
+ * one row range next to each other; inside its tile the byte of (row r,
+ * block b) is at (r % 32) * 16 + (r % 128) / 32 * 4 + b % 4.  Bytes of rows
+ * and blocks that do not exist are never used and never written.
+ *
+ * All pointers must be 16-byte aligned; sizes are at least 1 (rows and B
+ * included).  `ws` is scratch as above, of the bytes that the operator's
+ * _workspace_bytes call gives (0 for sizes that it refuses); it carries
+ * nothing from one call to the next, but two calls whose work overlaps on the
+ * GPU each need their own.  Its first int is the status of the call's bounded
+ * waits: 0, or bit 0 set (ALEXNET_ERR_TIMEOUT) with outputs not valid.
+ * Outputs do not overlap inputs or each other unless stated. */
+typedef enum { ALEXNET_E4M3 = 0, ALEXNET_E5M2 = 1 } alexnet_f8;
+typedef enum {
+  ALEXNET_SILU = 0, /* a(g) = g / (1 + exp(-g)) */
+  ALEXNET_GELU = 1, /* a(g) = g/2 (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) */
+  ALEXNET_RELU = 2  /* a(g) = max(g, 0), derivative 0 at 0 */
+} alexnet_act;
+
+/* Bytes of the scales of an 8-bit matrix: 512 * ceil(rows / 128) *
+ * ceil(cols / 512); 0 for rows or cols < 1 or cols % 16 != 0. */
+ALEXNET_API size_t alexnet_f8_scale_bytes(int64_t rows, int cols);
+
+/* bf16 [rows, cols] -> 8-bit rows of type fmt (alexnet_f8), and back to bf16
+ * (exact but for values under bf16's normal range, which are rounded, and
+ * 2^128, which becomes an infinity). */
+ALEXNET_API alexnet_status alexnet_op_f8_quant(const void* x, int64_t rows, int cols, int fmt,
+                                               void* q, uint8_t* scales, void* stream);
+ALEXNET_API alexnet_status alexnet_op_f8_dequant(const void* q, const uint8_t* scales,
+                                                 int64_t rows, int cols, int fmt, void* x,
+                                                 void* stream);
+
+/* Root-mean-square norm of rows, with the residual's addition:
+ *   s = x + res (rounded to bf16; s = x without res)
+ *   rstd = 1 / sqrt(mean(s^2) + eps);  y = s * rstd * gamma
+ * x, res (nullable) bf16 [rows, cols]; gamma fp32 [cols]; sum (nullable)
+ * bf16 receives s; y (nullable) bf16; rstd (nullable) fp32 [rows]; q and
+ * scales (both or neither) receive y, from its fp32 values, as E4M3 8-bit
+ * rows.  sum may be x or res itself.  cols % 8 == 0 (16 with q), cols <=
+ * 65536 (else UNSUPPORTED); eps > 0. */
+ALEXNET_API alexnet_status alexnet_op_rmsnorm_fwd(const void* x, const void* res,
+                                                  const float* gamma, int64_t rows, int cols,
+                                                  float eps, void* sum, void* y, float* rstd,
+                                                  void* q, uint8_t* scales, void* stream);
+
+/* Its gradient, from the stored s and rstd: with t = dy * gamma,
+ *   dx = rstd * (t - s * rstd^2 * mean(t * s)) + dsum
+ *   dgamma = sum over rows of dy * s * rstd   (fixed order: bit-reproducible)
+ * dx is the gradient of x and of res alike; dsum (nullable) bf16 is the
+ * gradient that reaches s from its other uses; dgamma nullable fp32 [cols].
+ * dx may be dy or dsum itself.  Sizes as the forward. */
+ALEXNET_API size_t alexnet_rmsnorm_workspace_bytes(int64_t rows, int cols);
+ALEXNET_API alexnet_status alexnet_op_rmsnorm_bwd(const void* dy, const void* dsum, const void* s,
+                                                  const float* gamma, const float* rstd,
+                                                  int64_t rows, int cols, void* dx, float* dgamma,
+                                                  void* ws, size_t ws_bytes, void* stream);
+
+/* Fully-connected product of 8-bit matrices, fp32 accumulation:
+ *   y[b,o] = sum_i x[b,i] w[o,i]
+ * x 8-bit rows [B, In] of type x_fmt with scales xs, w 8-bit rows [Out, In]
+ * of type w_fmt with scales wscales; y [B, Out] in y_dtype (alexnet_dtype).
+ * In % 16 == 0, Out % 8 == 0. */
+ALEXNET_API size_t alexnet_fc_f8_workspace_bytes(int B, int In, int Out);
+ALEXNET_API alexnet_status alexnet_op_fc_f8_fwd(const void* x, const uint8_t* xs, int x_fmt, int B,
+                                                int In, const void* w, const uint8_t* wscales,
+                                                int w_fmt, int Out, int y_dtype, void* y, void* ws,
+                                                size_t ws_bytes, void* stream);
+
+/* Gated feed-forward block: with w bf16 [2F, In], its first F rows the gate
+ * projection and its last F rows the up projection,
+ *   g = x wg^T, u = x wu^T (fp32);  h = a(g) * u
+ * x bf16 [B, In]; h bf16 [B, F]; act an alexnet_act; gu (nullable) [B, 2F]
+ * in gu_dtype (alexnet_dtype) receives g and u side by side for the backward
+ * pass: fp32 keeps them as they were summed, bf16 takes half the memory and
+ * adds its rounding to the gradients.  In % 8 == 0, F % 8 == 0. */
+ALEXNET_API size_t alexnet_gated_workspace_bytes(int B, int In, int F);
+ALEXNET_API alexnet_status alexnet_op_gated_fwd(const void* x, int B, int In, const void* w, int F,
+                                                int act, void* h, int gu_dtype, void* gu, void* ws,
+                                                size_t ws_bytes, void* stream);
+
+/* Its gradient: with dg = dh * u * a'(g) and du = dh * a(g), both rounded to
+ * bf16 for the products,
+ *   dx = dg wg + du wu;  dw = [dg du]^T x
+ * dh bf16 [B, F]; gu as the forward stored it; dx (nullable) bf16 [B, In];
+ * dw (nullable) bf16 [2F, In]. */
+ALEXNET_API alexnet_status alexnet_op_gated_bwd(const void* dh, const void* x, int gu_dtype,
+                                                const void* gu, int B, int In, const void* w,
+                                                int F, int act, void* dx, void* dw, void* ws, size_t ws_bytes,
+                                                void* stream);
+
+/* The same pair with 8-bit activation checkpoints (E4M3 8-bit rows) between
+ * the passes: the forward stores g and u as two 8-bit matrices [B, F] one
+ * after the other (guq 2*B*F bytes, gus 2 * alexnet_f8_scale_bytes(B, F)), h
+ * is computed from the unrounded g and u; the backward reads them and the
+ * 8-bit rows xq, xs of x [B, In] (alexnet_op_f8_quant, or the norm's output)
+ * and uses their values in the place of g, u and x.  In % 16 == 0, F % 16
+ * == 0; the workspace as above. */
+ALEXNET_API alexnet_status alexnet_op_gated_fwd_ckpt8(const void* x, int B, int In, const void* w,
+                                                      int F, int act, void* h, void* guq,
+                                                      uint8_t* gus, void* ws, size_t ws_bytes,
+                                                      void* stream);
+ALEXNET_API alexnet_status alexnet_op_gated_bwd_ckpt8(const void* dh, const void* xq,
+                                                      const uint8_t* xs, const void* guq,
+                                                      const uint8_t* gus, int B, int In,
+                                                      const void* w, int F, int act, void* dx,
+                                                      void* dw, void* ws, size_t ws_bytes,
+                                                      void* stream);
+
 /* Which kernel runs convolution `layer` (0..4) for a batch of `batch`
  * images: pass 0 forward, 1 data gradient (layers 1..4), 2 weight gradient.
  * *algo = 1: the shifted-box kernel (one input box per 64-channel chunk for
