@@ -275,11 +275,13 @@ def _own(s):
     if "work" not in s:
         s["work"] = torch.empty(ax.gated_workspace_bytes(B, In, F), dtype=torch.uint8, device="cuda")
     if op == "gated":
-        ax.op_gated_fwd(s["x"], B, In, s["w"], F, act, s["h"], None, s["work"])
+        ax.op_gated_fwd(s["x"], B, In, s["w"], F, act, s["h"], ax.FP32, None, s["work"])
         return s["h"]
     if op == "gated_train":
-        ax.op_gated_fwd(s["x"], B, In, s["w"], F, act, s["h"], s["gu"], s["work"])
-        ax.op_gated_bwd(s["dh"], s["x"], s["gu"], B, In, s["w"], F, act, s["dx"], s["dw"], s["work"])
+        if s["gu"].dtype != torch.float32:  # kept as summed: bf16 would add its rounding to the gradients
+            s["gu"] = torch.empty(B, 2 * F, device="cuda")
+        ax.op_gated_fwd(s["x"], B, In, s["w"], F, act, s["h"], ax.FP32, s["gu"], s["work"])
+        ax.op_gated_bwd(s["dh"], s["x"], ax.FP32, s["gu"], B, In, s["w"], F, act, s["dx"], s["dw"], s["work"])
     else:
         ax.op_f8_quant(s["x"], B, In, ax.E4M3, s["xq"], s["xs"])
         ax.op_gated_fwd_ckpt8(s["x"], B, In, s["w"], F, act, s["h"], s["guq"], s["gus"], s["work"])
