@@ -1,0 +1,34 @@
+// ff_gemm.h -- the products of the feed-forward operators.  D[M, N] = A[M, K]
+// B[N, K]^T, fp32 accumulation, bf16 or 8-bit operands.
+#pragma once
+#include <cuda_runtime.h>
+#include <cstdint>
+
+#include "ff.h"
+
+namespace alx {
+
+// What a product does with its accumulators.
+enum FfOut : int {
+  FF_BF16 = 0,   // out bf16 [M, N]
+  FF_F32 = 1,    // out fp32 [M, N]
+  FF_GATED = 2,  // B holds gate and up rows: out = h bf16 [M, F], and `save`
+};
+
+struct FfProduct {
+  // operands: row-major with K (or, _mn: M / N) fastest, 16-byte aligned.
+  // f8: bytes with scale tiles, K fastest.
+  const void *a, *b;
+  int a_mn, b_mn;
+  int f8, a_e5m2, b_e5m2;
+  const uint8_t *a_scales, *b_scales;
+  int M, N, K;   // FF_GATED: N = F, and B has 2F rows
+  int out_kind;
+  void* out;
+  int act;
+  GateSave save;
+  int* status;   // bit 0: a bounded wait ran out;
+  int fresh;     // set it to 0 first
+};
+
+}  // namespace alx

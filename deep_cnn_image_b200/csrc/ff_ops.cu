@@ -6,7 +6,8 @@
 #include "alexnet_ops.h"
 #include "f8.cuh"
 #include "ff.h"
-#include "gemm.h"
+#include "ff_gemm.h"
+#include "ff_pair.h"
 
 using namespace alx;
 
@@ -33,31 +34,25 @@ bool gated_dims(int B, int In, int F, int step) {
   return B >= 1 && In >= 1 && F >= 1 && In % step == 0 && F % step == 0;
 }
 
-// D[M, N] = A[M, K] B[N, K]^T on the library's GEMM kernel
-alexnet_status gemm(const void* a, int amn, const void* b, int bmn, int M, int N, int K, int epi,
-                    void* out, int* status, cudaStream_t s) {
-  GemmDesc d;
-  memset(&d, 0, sizeof(d));
-  d.asrc = amn ? A_TMA_MN : A_TMA_K;
-  d.bsrc = bmn ? B_TMA_MN : B_TMA_K;
-  d.bn = 256;
-  d.args.M = M;
-  d.args.N = N;
-  d.args.Kblocks = (K + 63) / 64;
-  d.args.kb_per_split = d.args.Kblocks;
-  d.args.groups = 1;
-  d.args.epi = epi;
-  d.args.out = out;
-  d.args.ld_out = N;
-  d.args.status = status;
-  const bool ok =
-      (amn ? make_tmap_bf16(&d.tmA, a, M, K, 2ull * M, 64, 64)
-           : make_tmap_bf16(&d.tmA, a, K, M, 2ull * K, 64, 128)) &&
-      (bmn ? make_tmap_bf16(&d.tmB, b, N, K, 2ull * N, 64, 64)
-           : make_tmap_bf16(&d.tmB, b, K, N, 2ull * K, 64, 256));
-  if (!ok) return ALEXNET_ERR_INVALID_ARG;
-  if (!gemm_finalize(&d, ff_num_sms())) return ALEXNET_ERR_UNSUPPORTED;
-  return done(gemm_launch(d, s));
+alexnet_status product(const FfProduct& p, cudaStream_t s) {
+  if (static_cast<int64_t>((p.M + 127) / 128) * ((p.N + 127) / 128) > 0x7FFFFFFF)
+    return ALEXNET_ERR_UNSUPPORTED;
+  cudaError_t e = cudaSuccess;
+  if (!ff_pair_product(p, s, &e)) return ALEXNET_ERR_UNSUPPORTED;
+  return done(e);
+}
+
+// D[M, N] = A[M, K] B[N, K]^T of bf16 operands; the status word stays
+FfProduct bf16_product(const void* a, int a_mn, const void* b, int b_mn, int M, int N, int K,
+                       void* out, int* status) {
+  FfProduct p;
+  memset(&p, 0, sizeof(p));
+  p.a = a, p.a_mn = a_mn, p.b = b, p.b_mn = b_mn;
+  p.M = M, p.N = N, p.K = K;
+  p.out_kind = FF_BF16;
+  p.out = out;
+  p.status = status;
+  return p;
 }
 
 }  // namespace
@@ -117,7 +112,7 @@ alexnet_status alexnet_op_rmsnorm_bwd(const void* dy, const void* dsum, const vo
 
 size_t alexnet_fc_f8_workspace_bytes(int B, int In, int Out) {
   if (B < 1 || In < 1 || Out < 1 || In % 16 || Out % 8 || In > MAX_DIM || Out > MAX_DIM) return 0;
-  return 256 + up256(2ull * B * In) + up256(2ull * Out * In);
+  return 256;
 }
 
 alexnet_status alexnet_op_fc_f8_fwd(const void* x, const uint8_t* xs, int x_fmt, int B, int In,
@@ -130,20 +125,22 @@ alexnet_status alexnet_op_fc_f8_fwd(const void* x, const uint8_t* xs, int x_fmt,
     return ALEXNET_ERR_INVALID_ARG;
   if (In > MAX_DIM || Out > MAX_DIM) return ALEXNET_ERR_UNSUPPORTED;
   if (!ws || ws_bytes < alexnet_fc_f8_workspace_bytes(B, In, Out)) return ALEXNET_ERR_INVALID_ARG;
-  uint8_t* p = U8(ws) + 256;
-  bf16* xb = reinterpret_cast<bf16*>(p);
-  bf16* wb = reinterpret_cast<bf16*>(p + up256(2ull * B * In));
-  cudaStream_t s = cu(stream);
-  cudaMemsetAsync(ws, 0, 4, s);
-  if (cudaError_t e = launch_f8_dequant(U8(x), xs, B, In, x_fmt, xb, s)) return done(e);
-  if (cudaError_t e = launch_f8_dequant(U8(w), wscales, Out, In, w_fmt, wb, s)) return done(e);
-  return gemm(xb, 0, wb, 0, B, Out, In, y_dtype == ALEXNET_FP32 ? EPI_F32 : EPI_BF16, y,
-              static_cast<int*>(ws), s);
+  FfProduct p;
+  memset(&p, 0, sizeof(p));
+  p.a = x, p.b = w, p.f8 = 1;
+  p.a_e5m2 = x_fmt, p.b_e5m2 = w_fmt;
+  p.a_scales = xs, p.b_scales = wscales;
+  p.M = B, p.N = Out, p.K = In;
+  p.out_kind = y_dtype == ALEXNET_FP32 ? FF_F32 : FF_BF16;
+  p.out = y;
+  p.status = static_cast<int*>(ws);
+  p.fresh = 1;
+  return product(p, cu(stream));
 }
 
 size_t alexnet_gated_workspace_bytes(int B, int In, int F) {
   if (!gated_dims(B, In, F, 8) || In > MAX_DIM || F > MAX_DIM) return 0;
-  return 256 + up256(8ull * B * F) + up256(2ull * B * In);
+  return 256 + up256(4ull * B * F) + up256(2ull * B * In);
 }
 
 }  // extern "C"
@@ -169,11 +166,12 @@ GateSave save_of(const void* guq, const uint8_t* gus) {
 
 alexnet_status gated_fwd(const void* x, int B, int In, const void* w, int F, int act, void* h,
                          const GateSave& save, void* ws, cudaStream_t s) {
-  float* z = reinterpret_cast<float*>(U8(ws) + 256);
-  cudaMemsetAsync(ws, 0, 4, s);
-  if (alexnet_status e = gemm(x, 0, w, 0, B, 2 * F, In, EPI_F32, z, static_cast<int*>(ws), s))
-    return e;
-  return done(launch_gate_fwd(z, B, F, act, B16(h), save, s));
+  FfProduct p = bf16_product(x, 0, w, 0, B, F, In, h, static_cast<int*>(ws));
+  p.out_kind = FF_GATED;
+  p.act = act;
+  p.save = save;
+  p.fresh = 1;
+  return product(p, s);
 }
 
 alexnet_status gated_bwd(const void* dh, const void* x, const GateSave& save, int B, int In,
@@ -182,11 +180,11 @@ alexnet_status gated_bwd(const void* dh, const void* x, const GateSave& save, in
   bf16* dz = reinterpret_cast<bf16*>(U8(ws) + 256);
   cudaMemsetAsync(ws, 0, 4, s);
   if (cudaError_t e = launch_gate_bwd(B16(dh), save, B, F, act, dz, s)) return done(e);
+  int* status = static_cast<int*>(ws);
   if (dx)
-    if (alexnet_status e =
-            gemm(dz, 0, w, 1, B, In, 2 * F, EPI_BF16, dx, static_cast<int*>(ws), s))
+    if (alexnet_status e = product(bf16_product(dz, 0, w, 1, B, In, 2 * F, dx, status), s))
       return e;
-  return dw ? gemm(dz, 1, x, 1, 2 * F, In, B, EPI_BF16, dw, static_cast<int*>(ws), s) : ALEXNET_OK;
+  return dw ? product(bf16_product(dz, 1, x, 1, 2 * F, In, B, dw, status), s) : ALEXNET_OK;
 }
 
 }  // namespace
@@ -235,7 +233,7 @@ alexnet_status alexnet_op_gated_bwd_ckpt8(const void* dh, const void* xq, const 
     return ALEXNET_ERR_INVALID_ARG;
   if (In > MAX_DIM || F > MAX_DIM) return ALEXNET_ERR_UNSUPPORTED;
   if (!ws || ws_bytes < alexnet_gated_workspace_bytes(B, In, F)) return ALEXNET_ERR_INVALID_ARG;
-  bf16* xb = reinterpret_cast<bf16*>(U8(ws) + 256 + up256(8ull * B * F));
+  bf16* xb = reinterpret_cast<bf16*>(U8(ws) + 256 + up256(4ull * B * F));
   if (dw)
     if (cudaError_t e = launch_f8_dequant(U8(xq), xs, B, In, ALEXNET_E4M3, xb, cu(stream)))
       return done(e);

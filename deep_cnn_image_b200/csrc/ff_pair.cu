@@ -1,0 +1,521 @@
+// ff_pair.cu -- large products of the feed-forward operators: 256 x 256
+// output tiles by pairs of CTAs.
+//
+// A pair (two SMs) shares one tile: each CTA holds 128 rows of A and 128 of
+// the 256 rows of B in its shared memory, and tcgen05.mma.cta_group::2 reads
+// both halves of B, so per SM a 64-element (128-byte) step of K brings in
+// 32 KB for 2 x 128 x 256 x 64 products: half the operand traffic, from L2 and
+// in shared memory, of single-CTA 128 x 256 tiles.  Each CTA keeps its 128
+// rows of the accumulator in its own tensor memory, twice, so that one
+// tile's epilogue runs beside the next tile's products.
+//
+// Roles in a CTA (320 threads): warps 0-7 epilogue (TMEM -> registers ->
+// global; warp w reads lane quarter w % 4, warps 0-3 the lower half of the
+// columns), warp 8 TMA producer, warp 9 TMEM owner and, in the pair's rank 0,
+// MMA issuer.  The full barriers live in rank 0 (both CTAs' loads count their
+// bytes there); the empty and accumulator-full barriers are in both CTAs,
+// arrived at by a commit that reaches both.
+//
+// 8-bit operands: the scales of 128 rows and four 128-element blocks are one
+// 512-byte tile, loaded with every fourth stage and copied to tensor memory in
+// front of that stage's products, which pick the block's byte by their
+// instruction descriptor.  The tensor cores apply the scales; tiles, swizzle
+// and stages are the bf16 ones (a stage is 128 bytes of K either way).
+// Scales need 24 of the 512 columns, so the two accumulators overlap by 24
+// columns; the epilogue reads those first and then lets the next tile start.
+#include <cstring>
+
+#include "f8.cuh"
+#include "ff_gemm.h"
+#include "ff_pair.h"
+#include "gate.cuh"
+#include "gemm.h"
+#include "kernels.h"
+#include "tc2.cuh"
+
+namespace alx {
+
+namespace {
+
+constexpr int THREADS = 320;
+constexpr int HALF_BYTES = 128 * 128;       // one CTA's A or B rows of a stage
+constexpr int MN_BOX = 64 * 128;            // 64 K-rows x 64 bf16 elements
+constexpr int SCALE_BYTES = 3 * F8_TILE_BYTES;  // one A and two B tiles
+constexpr int ACC_WARPS = 16;               // epilogue warps of a pair
+
+struct PairArgs {
+  int M, N, kblocks;     // N: output columns (FF_GATED: F)
+  int m_tiles, n_tiles;  // of 256 rows; of 256 (FF_GATED: 128) columns
+  int k_tiles;           // scale tiles per 128 rows
+  int act, wide;         // wide: 32-byte stores are aligned
+  int fresh;             // clear the status word first
+  uint32_t idesc;
+  void* out;
+  GateSave save;
+  int* status;
+};
+
+// Tiles in bands of 8 rows of tiles, column by column inside a band: the
+// tiles that run at one time then share few rows of A and B, which stay in L2.
+__device__ __forceinline__ void tile_at(const PairArgs& a, int t, int& m, int& n) {
+  constexpr int BAND = 8;
+  const int per_band = BAND * a.n_tiles;
+  const int band = t / per_band;
+  const int rows = min(BAND, a.m_tiles - band * BAND);
+  const int r = t - band * per_band;
+  n = r / rows;
+  m = band * BAND + (r - n * rows);
+}
+
+// 16 columns of this warp's 32 lanes, not yet waited for.
+__device__ __forceinline__ void ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+// ties the loaded registers to the wait, so that no use moves in front of it
+__device__ __forceinline__ void ld_wait(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+
+// 16 columns of a row as bf16 or fp32; cols (> 0) of them exist, a multiple
+// of 8.
+__device__ __forceinline__ void put_bf16(bf16* p, const uint32_t (&r)[16], int cols, int wide) {
+  uint32_t o[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    o[i] = pack_bf16(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+  if (wide && cols >= 16) {
+    st32(p, o);
+  } else {
+    *reinterpret_cast<uint4*>(p) = make_uint4(o[0], o[1], o[2], o[3]);
+    if (cols > 8) *reinterpret_cast<uint4*>(p + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+  }
+}
+__device__ __forceinline__ void put_f32(float* p, const uint32_t (&r)[16], int cols, int wide) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (8 * h >= cols) break;
+    const uint32_t o[8] = {r[8 * h],     r[8 * h + 1], r[8 * h + 2], r[8 * h + 3],
+                           r[8 * h + 4], r[8 * h + 5], r[8 * h + 6], r[8 * h + 7]};
+    if (wide) {
+      st32(p + 8 * h, o);
+    } else {
+      *reinterpret_cast<uint4*>(p + 8 * h) = make_uint4(o[0], o[1], o[2], o[3]);
+      *reinterpret_cast<uint4*>(p + 8 * h + 4) = make_uint4(o[4], o[5], o[6], o[7]);
+    }
+  }
+}
+
+// One projection of a row (128 columns at taddr, `cols` of them real) as
+// 8-bit codes: the largest magnitude first, then the codes.  Every lane of
+// the warp takes part in the loads.
+__device__ __forceinline__ void put_codes(uint32_t taddr, int cols, bool live, uint8_t* q,
+                                          uint8_t* scale, int wide) {
+  float a = 0.f;
+#pragma unroll 1
+  for (int c = 0; c < 128; c += 16) {
+    __syncwarp();
+    uint32_t r[16];
+    ld16(taddr + c, r);
+    ld_wait(r);
+    if (c < cols) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) a = fmaxf(a, fabsf(f8_finite(__uint_as_float(r[i]))));
+    }
+  }
+  const uint32_t s = f8_scale_byte(a, 0);
+  const float inv = f8_scale_inv(s);
+  if (live) *scale = static_cast<uint8_t>(s);
+#pragma unroll 1
+  for (int c = 0; c < 128; c += 32) {
+    __syncwarp();
+    uint32_t r0[16], r1[16], o[8];
+    ld16(taddr + c, r0);
+    ld16(taddr + c + 16, r1);
+    ld_wait(r0);
+    ld_wait(r1);
+    if (!live || c >= cols) continue;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[j] = f8_finite(__uint_as_float(r0[4 * i + j])) * inv;
+        v[4 + j] = f8_finite(__uint_as_float(r1[4 * i + j])) * inv;
+      }
+      o[i] = f8_pack4(v[0], v[1], v[2], v[3], 0);
+      o[4 + i] = f8_pack4(v[4], v[5], v[6], v[7], 0);
+    }
+    if (wide && c + 32 <= cols) {
+      st32(q + c, o);
+    } else {
+      *reinterpret_cast<uint4*>(q + c) = make_uint4(o[0], o[1], o[2], o[3]);
+      if (c + 16 < cols) *reinterpret_cast<uint4*>(q + c + 16) = make_uint4(o[4], o[5], o[6], o[7]);
+    }
+  }
+}
+
+template <int F8, int A_MN, int B_MN, int OUT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+    k_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+           const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
+           const __grid_constant__ PairArgs args, int stages) {
+  constexpr int STAGE_SCALES = F8 ? SCALE_BYTES : 0;
+  constexpr uint32_t ACC_STEP = F8 ? 232 : 256;  // columns between the accumulators
+  constexpr uint32_t SCALE_COL = 488;
+  constexpr int ROW_TILE_N = OUT == FF_GATED ? 128 : 256;
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t sA = smem_u32(smem);
+  const uint32_t sB = sA + stages * HALF_BYTES;
+  const uint32_t sS = sB + stages * HALF_BYTES;
+  uint64_t* bars =
+      reinterpret_cast<uint64_t*>(smem + stages * (2 * HALF_BYTES + STAGE_SCALES));
+  const uint32_t bar_full = smem_u32(bars);
+  const uint32_t bar_empty = bar_full + 8 * stages;
+  const uint32_t bar_acc_full = bar_full + 16 * stages;
+  const uint32_t bar_acc_empty = bar_acc_full + 16;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * stages + 4);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+
+  if (threadIdx.x == 0) {
+    if (args.fresh && blockIdx.x == 0) *args.status = 0;
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(bar_full + 8 * s, 1);
+      mbar_init(bar_empty + 8 * s, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar_acc_full + 8 * i, 1);
+      mbar_init(bar_acc_empty + 8 * i, ACC_WARPS);
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 9) tmem_alloc_pair(smem_u32(tmem_slot), 512);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  const int total = args.m_tiles * args.n_tiles;
+  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+
+  if (warp == 8) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      tma_prefetch_desc(&tmA);
+      tma_prefetch_desc(&tmB);
+      const uint32_t full0 = map_rank(bar_full, 0);
+      RingPos r;
+      int loaded = 0;
+      bool ok = true;
+      for (int t = first; t < total && ok; t += step) {
+        int m, n;
+        tile_at(args, t, m, n);
+        const int m0 = m * 256 + rank * 128;
+        // FF_GATED: rank 0 brings gate rows, rank 1 the up rows beside them
+        const int n0 = OUT == FF_GATED ? n * 128 + static_cast<int>(rank) * args.N
+                                       : n * 256 + static_cast<int>(rank) * 128;
+        for (int kb = 0; kb < args.kblocks; ++kb, r.next(stages), ++loaded) {
+          const uint32_t s = r.slot;
+          if (!mbar_wait(bar_empty + 8 * s, r.phase ^ 1, args.status, abort_flag)) {
+            ok = false;
+            break;
+          }
+          const bool with_scales = F8 && (kb & 3) == 0;
+          if (rank == 0)
+            mbar_arrive_expect_tx(bar_full + 8 * s,
+                                  4 * HALF_BYTES + (with_scales ? 2 * SCALE_BYTES : 0));
+          const uint32_t fb = full0 + 8 * s;
+          const uint32_t dA = sA + s * HALF_BYTES, dB = sB + s * HALF_BYTES;
+          if (A_MN) {
+            tma_load_2d_pair(dA, &tmA, m0, kb * 64, fb);
+            tma_load_2d_pair(dA + MN_BOX, &tmA, m0 + 64, kb * 64, fb);
+          } else {
+            tma_load_2d_pair(dA, &tmA, kb * 64, m0, fb);
+          }
+          if (B_MN) {
+            tma_load_2d_pair(dB, &tmB, n0, kb * 64, fb);
+            tma_load_2d_pair(dB + MN_BOX, &tmB, n0 + 64, kb * 64, fb);
+          } else {
+            tma_load_2d_pair(dB, &tmB, kb * 64, n0, fb);
+          }
+          if (with_scales) {
+            const uint32_t dS = sS + s * SCALE_BYTES;
+            const int kt = kb >> 2;
+            tma_load_2d_pair(dS, &tmSA, 0, (m * 2 + rank) * args.k_tiles + kt, fb);
+            tma_load_2d_pair(dS + F8_TILE_BYTES, &tmSB, 0, (n * 2) * args.k_tiles + kt, fb);
+            tma_load_2d_pair(dS + 2 * F8_TILE_BYTES, &tmSB, 0, (n * 2 + 1) * args.k_tiles + kt, fb);
+          }
+        }
+      }
+      // the commits that free the last stages arrive here too: wait for them,
+      // so that none reaches this CTA's shared memory after it has ended
+      if (loaded < stages) r = RingPos{};
+      for (int i = 0; i < min(stages, loaded) && ok; ++i, r.next(stages))
+        ok = mbar_wait(bar_empty + 8 * r.slot, loaded < stages ? 0 : r.phase ^ 1, args.status,
+                       abort_flag);
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ MMA issuer
+    if (rank == 0 && lane == 0) {
+      const uint64_t a0 = A_MN ? smem_desc_sw128(sA, MN_BOX, 1024) : smem_desc_sw128(sA, 16, 1024);
+      const uint64_t b0 = B_MN ? smem_desc_sw128(sB, MN_BOX, 1024) : smem_desc_sw128(sB, 16, 1024);
+      const uint32_t a_lo = static_cast<uint32_t>(a0), a_hi = static_cast<uint32_t>(a0 >> 32);
+      const uint32_t b_lo = static_cast<uint32_t>(b0), b_hi = static_cast<uint32_t>(b0 >> 32);
+      constexpr int AS = A_MN ? 128 : 2, BS = B_MN ? 128 : 2;  // 16-byte units per MMA step
+      RingPos r;
+      uint32_t count = 0, scale_buf = 0;
+      bool ok = true;
+      for (int t = first; t < total && ok; t += step, ++count) {
+        const uint32_t acc = count & 1;
+        if (F8) {
+          // the tile before this one has left the columns the two share
+          if (count && !mbar_wait_cluster(bar_acc_empty + 8 * acc, ((count - 1) >> 1) & 1,
+                                          args.status, abort_flag))
+            break;
+        } else if (!mbar_wait_cluster(bar_acc_empty + 8 * acc, ((count >> 1) & 1) ^ 1, args.status,
+                                      abort_flag)) {
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem_base + acc * ACC_STEP;
+        uint32_t sa = 0, sb = 0;
+        for (int kb = 0; kb < args.kblocks; ++kb, r.next(stages)) {
+          const uint32_t s = r.slot;
+          if (!mbar_wait(bar_full + 8 * s, r.phase, args.status, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (F8 && (kb & 3) == 0) {
+            sa = tmem_base + SCALE_COL + 12 * scale_buf;
+            sb = sa + 4;
+            scale_buf ^= 1;
+            const uint32_t dS = sS + s * SCALE_BYTES;
+            copy_scales<1>(sa, scale_desc(dS));
+            copy_scales<1>(sb, scale_desc(dS + F8_TILE_BYTES));
+            copy_scales<1>(sb + 4, scale_desc(dS + 2 * F8_TILE_BYTES));
+          }
+          const uint32_t al = a_lo + s * (HALF_BYTES >> 4), bl = b_lo + s * (HALF_BYTES >> 4);
+          const uint32_t idesc = F8 ? args.idesc | idesc_f8_byte(kb & 3) : args.idesc;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint64_t da = desc_at(a_hi, al + k * AS), db = desc_at(b_hi, bl + k * BS);
+            const uint32_t keep = (kb | k) ? 1u : 0u;
+            if (F8)
+              mma_f8<1>(d, da, db, idesc, sa, sb, keep);
+            else
+              mma_bf16<1>(d, da, db, idesc, keep);
+          }
+          tc_commit_pair(bar_empty + 8 * s);
+        }
+        if (!ok) break;
+        tc_commit_pair(bar_acc_full + 8 * acc);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int quarter = warp & 3, half = warp >> 2;
+    const uint32_t empty0 = map_rank(bar_acc_empty, 0);
+    uint32_t count = 0;
+    for (int t = first; t < total; t += step, ++count) {
+      int m, n;
+      tile_at(args, t, m, n);
+      const uint32_t acc = count & 1;
+      if (!mbar_wait(bar_acc_full + 8 * acc, (count >> 1) & 1, args.status, abort_flag)) break;
+      tc_fence_after();
+      const int64_t row = static_cast<int64_t>(m) * 256 + rank * 128 + quarter * 32 + lane;
+      const bool live = row < args.M;
+      const uint32_t tb =
+          tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * ACC_STEP;
+      auto leave = [&](uint32_t which) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(empty0 + 8 * which);
+      };
+      const int n0 = n * ROW_TILE_N;
+      if (OUT == FF_GATED) {
+        const int F = args.N;
+        bf16* h = static_cast<bf16*>(args.out) + row * F + n0;
+        const GateSave& sv = args.save;
+#pragma unroll 1
+        for (int c = half * 64; c < half * 64 + 64; c += 16) {
+          __syncwarp();
+          uint32_t g[16], u[16], o[16];
+          ld16(tb + c, g);
+          ld16(tb + 128 + c, u);
+          ld_wait(g);
+          ld_wait(u);
+          const int cols = F - n0 - c;
+          if (!live || cols <= 0) continue;
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            o[i] = __float_as_uint(gate_value(__uint_as_float(g[i]), args.act) *
+                                   __uint_as_float(u[i]));
+          put_bf16(h + c, o, cols, args.wide);
+          if (sv.f32) {
+            float* p = sv.f32 + row * 2 * F + n0 + c;
+            put_f32(p, g, cols, args.wide);
+            put_f32(p + F, u, cols, args.wide);
+          } else if (sv.b16) {
+            bf16* p = sv.b16 + row * 2 * F + n0 + c;
+            put_bf16(p, g, cols, args.wide);
+            put_bf16(p + F, u, cols, args.wide);
+          }
+        }
+        if (sv.q) {
+          // one half of the warps takes g, the other u
+          const int ct = (F + F8_TILE_COLS - 1) / F8_TILE_COLS;
+          const size_t each = static_cast<size_t>((args.M + 127) / 128) * ct * F8_TILE_BYTES;
+          uint8_t* q = sv.q + (half * static_cast<int64_t>(args.M) + row) * F + n0;
+          put_codes(tb + 128 * half, F - n0, live, q,
+                    sv.qs + half * each + f8_scale_at(row, n, ct), args.wide && F % 32 == 0);
+        }
+        leave(acc);
+      } else {
+        // 8-bit operands: columns 232-255 of the first accumulator are columns
+        // 0-23 of the second.  The warps that hold them read them first, and
+        // the next tile may start when all have; a tile's own rest is read by
+        // the time that the tile after the next one asks.
+        const bool shares = F8 && half == (acc ? 0 : 1);
+        const bool down = F8 && acc == 0;
+        if (F8 && !shares) leave(acc ^ 1);
+#pragma unroll 1
+        for (int i = 0; i < 8; i += 2) {
+          __syncwarp();
+          uint32_t r0[16], r1[16];
+          const int c = half * 128 + (down ? 96 - i * 16 : i * 16);
+          ld16(tb + c, r0);
+          ld16(tb + c + 16, r1);
+          ld_wait(r0);
+          ld_wait(r1);
+          if (shares && i == 0) leave(acc ^ 1);
+          const int cols = args.N - n0 - c;
+          if (!live || cols <= 0) continue;
+          if (OUT == FF_BF16) {
+            bf16* p = static_cast<bf16*>(args.out) + row * args.N + n0 + c;
+            put_bf16(p, r0, cols, args.wide);
+            if (cols > 16) put_bf16(p + 16, r1, cols - 16, args.wide);
+          } else {
+            float* p = static_cast<float*>(args.out) + row * args.N + n0 + c;
+            put_f32(p, r0, cols, args.wide);
+            if (cols > 16) put_f32(p + 16, r1, cols - 16, args.wide);
+          }
+        }
+        if (!F8) leave(acc);
+      }
+    }
+  }
+
+  __syncthreads();
+  if (*abort_flag) {
+    // give bulk copies already in flight time to land before the CTA ends
+    for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+  }
+  cluster_sync();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, 512);
+  }
+}
+
+template <int F8, int A_MN, int B_MN, int OUT>
+cudaError_t launch(const CUtensorMap (&tm)[4], const PairArgs& a, int stages, int smem, int grid,
+                   cudaStream_t s) {
+  static bool ready[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !ready[dev]) {
+    if (cudaError_t e = cudaFuncSetAttribute(k_pair<F8, A_MN, B_MN, OUT>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             227 * 1024))
+      return e;
+    if (dev >= 0 && dev < 64) ready[dev] = true;
+  }
+  count_launch();
+  k_pair<F8, A_MN, B_MN, OUT><<<grid, THREADS, smem, s>>>(tm[0], tm[1], tm[2], tm[3], a, stages);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+bool ff_pair_product(const FfProduct& p, cudaStream_t s, cudaError_t* err) {
+  CUtensorMap tm[4];
+  memset(tm, 0, sizeof(tm));
+  const bool gated = p.out_kind == FF_GATED;
+  const int brows = gated ? 2 * p.N : p.N;
+  // 8-bit rows are mapped as rows of half as many 2-byte elements
+  const int K = p.f8 ? p.K / 2 : p.K;
+  const bool ok =
+      (p.a_mn ? make_tmap_bf16(&tm[0], p.a, p.M, K, 2ull * p.M, 64, 64)
+              : make_tmap_bf16(&tm[0], p.a, K, p.M, 2ull * K, 64, 128)) &&
+      (p.b_mn ? make_tmap_bf16(&tm[1], p.b, p.N, K, 2ull * p.N, 64, 64)
+              : make_tmap_bf16(&tm[1], p.b, K, brows, 2ull * K, 64, 128));
+  if (!ok) return false;
+  PairArgs a;
+  memset(&a, 0, sizeof(a));
+  a.M = p.M;
+  a.N = p.N;
+  a.kblocks = (K + 63) / 64;
+  a.m_tiles = (p.M + 255) / 256;
+  a.n_tiles = gated ? (p.N + 127) / 128 : (p.N + 255) / 256;
+  a.act = p.act;
+  a.out = p.out;
+  a.save = p.save;
+  a.status = p.status;
+  a.fresh = p.fresh;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p.out) |
+                       reinterpret_cast<uintptr_t>(p.save.f32) |
+                       reinterpret_cast<uintptr_t>(p.save.b16) |
+                       reinterpret_cast<uintptr_t>(p.save.q);
+  a.wide = at % 32 == 0 && p.N % 16 == 0;
+  if (p.f8) {
+    a.k_tiles = (p.K + F8_TILE_COLS - 1) / F8_TILE_COLS;
+    if (!make_tmap_u32(&tm[2], p.a_scales, 128, static_cast<uint64_t>((p.M + 127) / 128) * a.k_tiles,
+                       128, 1) ||
+        !make_tmap_u32(&tm[3], p.b_scales, 128, static_cast<uint64_t>((p.N + 127) / 128) * a.k_tiles,
+                       128, 1))
+      return false;
+    a.idesc = idesc_f8(256, 256, p.a_e5m2, p.b_e5m2);
+  } else {
+    a.idesc = idesc_bf16(256, 256, p.a_mn, p.b_mn);
+  }
+  const int stages = p.f8 ? 6 : 7;
+  const int smem = stages * (2 * HALF_BYTES + (p.f8 ? SCALE_BYTES : 0)) + 1024 + 256;
+  const int pairs = ff_num_sms() / 2;
+  const int tiles = a.m_tiles * a.n_tiles;
+  const int grid = 2 * (tiles < pairs ? tiles : pairs);
+#define ALX_PAIR(F8_, AM_, BM_, OUT_)                                              \
+  if (p.f8 == F8_ && p.a_mn == AM_ && p.b_mn == BM_ && p.out_kind == OUT_) {       \
+    *err = launch<F8_, AM_, BM_, OUT_>(tm, a, stages, smem, grid, s);              \
+    return true;                                                                   \
+  }
+  ALX_PAIR(0, 0, 0, FF_GATED)
+  ALX_PAIR(0, 0, 1, FF_BF16)
+  ALX_PAIR(0, 1, 1, FF_BF16)
+  ALX_PAIR(1, 0, 0, FF_BF16)
+  ALX_PAIR(1, 0, 0, FF_F32)
+#undef ALX_PAIR
+  return false;
+}
+
+}  // namespace alx

@@ -96,6 +96,11 @@ struct GemmDesc {
 bool make_tmap_bf16(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer,
                     uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer);
 
+// 2-D map of 32-bit words without swizzle: rows of `inner` words, one after
+// the other, `outer` of them; box of box_inner x box_outer.
+bool make_tmap_u32(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer,
+                   uint32_t box_inner, uint32_t box_outer);
+
 // 4-D tiled tensor map over an NHWC bf16 tensor [N, H, W, C] (dimensions in
 // (C, W, H, N) order), box box_c x box_w x box_h x 1, 128-byte swizzle
 // (box_c * 2 <= 128).  Out-of-range box elements read as zero.
