@@ -10,8 +10,46 @@ namespace alx {
 
 using bf16 = __nv_bfloat16;
 
-// the attributes of the device that is current (cached per device)
+// SMs of the device that is current (cached per device)
 int ff_num_sms();
+
+// Launch with programmatic stream serialisation: the kernel may start, and set
+// up its barriers and tensor memory, while the one before it in the stream
+// ends.  Every kernel launched so calls grid_dep_wait before it reads or
+// writes memory, which returns once all earlier work of the stream is done
+// and visible.  cluster: CTAs per cluster (0: the kernel's own).
+template <typename... P, typename... A>
+cudaError_t ff_launch(void (*kernel)(P...), int64_t grid, int block, int smem, int cluster,
+                      cudaStream_t stream, A&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
+// Lets a kernel use all of an SM's shared memory; once per kernel and device.
+template <typename K>
+cudaError_t ff_all_smem(K kernel, bool (&ready)[64]) {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const bool known = dev >= 0 && dev < 64;
+  if (known && ready[dev]) return cudaSuccess;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+  if (known && e == cudaSuccess) ready[dev] = true;
+  return e;
+}
 
 // rmsnorm.cu
 constexpr int RMSNORM_MAX_COLS = 65536;
@@ -39,8 +77,8 @@ struct GateSave {
 // z fp32 [B, 2F] -> h, and z in what `save` holds
 cudaError_t launch_gate_fwd(const float* z, int B, int F, int act, bf16* h, const GateSave& save,
                             cudaStream_t s);
-// dz bf16 [B, 2F] from dh and the saved projections
+// dz bf16 [B, 2F] from dh and the saved projections; *status = 0
 cudaError_t launch_gate_bwd(const bf16* dh, const GateSave& save, int B, int F, int act, bf16* dz,
-                            cudaStream_t s);
+                            int* status, cudaStream_t s);
 
 }  // namespace alx

@@ -31,4 +31,22 @@ struct FfProduct {
   int fresh;     // set it to 0 first
 };
 
+// Both run the product and set *err to the launch's error; false where the
+// operands cannot be mapped or no operator uses the combination of layouts.
+// Large products, on pairs of CTAs (ff_pair.cu):
+bool ff_pair_product(const FfProduct& p, cudaStream_t s, cudaError_t* err);
+// few rows of A (ff_narrow.cu); does not keep 8-bit projections:
+bool ff_narrow_product(const FfProduct& p, cudaStream_t s, cudaError_t* err);
+
+// How a narrow product is cut up: tiles of 128 weight rows by up to 128
+// (bn) tokens, each split over a cluster of `split` CTAs; `ns`: its expected
+// time.
+struct FfNarrowPlan {
+  int bn, tiles, split;
+  double ns;
+};
+FfNarrowPlan ff_narrow_plan(int tokens, int rows, int kblocks);
+// the expected time of the same product on pairs of CTAs
+double ff_pair_ns(int tokens, int rows, int kblocks);
+
 }  // namespace alx

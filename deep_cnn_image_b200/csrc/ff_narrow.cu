@@ -1,0 +1,413 @@
+// ff_narrow.cu -- products of the feed-forward operators with few rows of
+// activations, down to a single token.
+//
+// Such a product is bound by reading the weights once.  The weights' rows
+// therefore take the M side of the tensor-core tile (128 of them; for the
+// gated block 64 gate rows and the 64 up rows that belong to them), the
+// tokens the N side (16, 32, 64 or 128), and the grid is (weight tiles) x
+// (token tiles) x S: a cluster of S <= 8 CTAs splits the reduction of one tile,
+// so that all SMs stream weights even where there are few tiles.  Each CTA
+// runs its slice of K through a ring of TMA stages into one accumulator in
+// tensor memory, puts it into its shared memory as [token][row], and the
+// cluster's CTAs add up the S copies through distributed shared memory, each
+// for its share of the tokens, in a fixed order; no partial sum reaches
+// memory and nothing depends on timing.  Rows of the weights are consecutive
+// columns of the result, so a token's 128 results leave as one run.
+//
+// Roles (320 threads): warps 0-7 epilogue, warp 8 TMA producer, warp 9 MMA
+// issuer and TMEM owner.
+#include <cstring>
+
+#include "f8.cuh"
+#include "ff_gemm.h"
+#include "gate.cuh"
+#include "gemm.h"
+#include "kernels.h"
+#include "tc2.cuh"
+
+namespace alx {
+
+namespace {
+
+constexpr int THREADS = 320;
+constexpr int W_BYTES = 128 * 128;      // weight rows of a stage
+constexpr int BOX_BYTES = 64 * 128;     // one of its two boxes
+constexpr int SCALES = 2 * F8_TILE_BYTES;
+
+struct NarrowArgs {
+  int tokens, rows;        // rows: output columns (gated: F)
+  int kblocks, per;        // 128-byte steps of K, and how many a CTA takes
+  int token_tiles;
+  int k_tiles;             // scale tiles per 128 rows
+  int act;
+  int fresh;
+  uint32_t idesc;
+  void* out;
+  GateSave save;
+  int* status;
+};
+
+// a += b
+__device__ __forceinline__ void add4(float4& a, const float4& b) {
+  a.x += b.x;
+  a.y += b.y;
+  a.z += b.z;
+  a.w += b.w;
+}
+__device__ __forceinline__ void put4(float* p, const float4& v) {
+  *reinterpret_cast<float4*>(p) = v;
+}
+__device__ __forceinline__ void put4(bf16* p, const float4& v) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+}
+__device__ __forceinline__ float4 gate4(const float4& g, const float4& u, int act) {
+  return make_float4(gate_value(g.x, act) * u.x, gate_value(g.y, act) * u.y,
+                     gate_value(g.z, act) * u.z, gate_value(g.w, act) * u.w);
+}
+
+// W_MN: the weights are stored with their rows (the M side) fastest.
+template <int F8, int W_MN, int BN, int OUT>
+__global__ void __launch_bounds__(THREADS)
+    k_narrow(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+             const __grid_constant__ CUtensorMap tmSW, const __grid_constant__ CUtensorMap tmSX,
+             const __grid_constant__ NarrowArgs args, int stages, int S) {
+  constexpr int X_BYTES = BN * 128;
+  constexpr int STAGE_SCALES = F8 ? SCALES : 0;
+  constexpr bool GATED = OUT == FF_GATED;
+  constexpr uint32_t ACC_COLS = BN < 32 ? 32 : BN;
+  constexpr uint32_t TMEM_COLS = F8 ? (BN == 128 ? 256 : (BN == 64 ? 128 : 64)) : ACC_COLS;
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t sW = smem_u32(smem);
+  const uint32_t sX = sW + stages * W_BYTES;
+  const uint32_t sS = sX + stages * X_BYTES;
+  uint64_t* bars =
+      reinterpret_cast<uint64_t*>(smem + stages * (W_BYTES + X_BYTES + STAGE_SCALES));
+  const uint32_t bar_full = smem_u32(bars);
+  const uint32_t bar_empty = bar_full + 8 * stages;
+  const uint32_t bar_acc = bar_full + 16 * stages;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * stages + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int rank = blockIdx.x % S;
+  const int tile = blockIdx.x / S;
+  const int tt = tile % args.token_tiles, wt = tile / args.token_tiles;
+  const int kb0 = rank * args.per;
+  const int kb1 = min(args.kblocks, kb0 + args.per);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(bar_full + 8 * s, 1);
+      mbar_init(bar_empty + 8 * s, 1);
+    }
+    mbar_init(bar_acc, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 9) {
+    tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  if (warp == 8 && lane == 0) {
+    tma_prefetch_desc(&tmW);
+    tma_prefetch_desc(&tmX);
+    if (F8) {
+      tma_prefetch_desc(&tmSW);
+      tma_prefetch_desc(&tmSX);
+    }
+  }
+  grid_dep_launch();
+  grid_dep_wait();
+  if (args.fresh && blockIdx.x == 0 && threadIdx.x == 0) *args.status = 0;
+
+  if (warp == 8) {
+    if (lane == 0) {
+      RingPos r;
+      const int w0 = GATED ? wt * 64 : wt * 128;
+      const int w1 = GATED ? args.rows + w0 : w0 + 64;
+      for (int kb = kb0; kb < kb1; ++kb, r.next(stages)) {
+        const uint32_t s = r.slot;
+        if (!mbar_wait(bar_empty + 8 * s, r.phase ^ 1, args.status, abort_flag)) break;
+        const uint32_t fb = bar_full + 8 * s;
+        const bool with_scales = F8 && (kb == kb0 || (kb & 3) == 0);
+        mbar_arrive_expect_tx(fb, W_BYTES + X_BYTES + (with_scales ? SCALES : 0));
+        const uint32_t dW = sW + s * W_BYTES;
+        if (W_MN) {
+          tma_load_2d(dW, &tmW, w0, kb * 64, fb);
+          tma_load_2d(dW + BOX_BYTES, &tmW, w1, kb * 64, fb);
+        } else {
+          tma_load_2d(dW, &tmW, kb * 64, w0, fb);
+          tma_load_2d(dW + BOX_BYTES, &tmW, kb * 64, w1, fb);
+        }
+        tma_load_2d(sX + s * X_BYTES, &tmX, kb * 64, tt * BN, fb);
+        if (with_scales) {
+          const uint32_t dS = sS + s * SCALES;
+          tma_load_2d(dS, &tmSW, 0, wt * args.k_tiles + (kb >> 2), fb);
+          tma_load_2d(dS + F8_TILE_BYTES, &tmSX, 0, tt * args.k_tiles + (kb >> 2), fb);
+        }
+      }
+    }
+  } else if (warp == 9) {
+    if (lane == 0) {
+      const uint64_t a0 =
+          W_MN ? smem_desc_sw128(sW, BOX_BYTES, 1024) : smem_desc_sw128(sW, 16, 1024);
+      const uint64_t b0 = smem_desc_sw128(sX, 16, 1024);
+      const uint32_t a_lo = static_cast<uint32_t>(a0), a_hi = static_cast<uint32_t>(a0 >> 32);
+      const uint32_t b_lo = static_cast<uint32_t>(b0), b_hi = static_cast<uint32_t>(b0 >> 32);
+      constexpr int AS = W_MN ? 128 : 2;
+      RingPos r;
+      uint32_t scale_buf = 0, sa = 0;
+      bool ok = true;
+      for (int kb = kb0; kb < kb1; ++kb, r.next(stages)) {
+        const uint32_t s = r.slot;
+        if (!mbar_wait(bar_full + 8 * s, r.phase, args.status, abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (F8 && (kb == kb0 || (kb & 3) == 0)) {
+          sa = tmem_base + ACC_COLS + 8 * scale_buf;
+          scale_buf ^= 1;
+          copy_scales<0>(sa, scale_desc(sS + s * SCALES));
+          copy_scales<0>(sa + 4, scale_desc(sS + s * SCALES + F8_TILE_BYTES));
+        }
+        const uint32_t al = a_lo + s * (W_BYTES >> 4), bl = b_lo + s * (X_BYTES >> 4);
+        const uint32_t idesc = F8 ? args.idesc | idesc_f8_byte(kb & 3) : args.idesc;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint64_t da = desc_at(a_hi, al + k * AS), db = desc_at(b_hi, bl + k * 2);
+          const uint32_t keep = (kb > kb0 || k) ? 1u : 0u;
+          if (F8)
+            mma_f8<0>(tmem_base, da, db, idesc, sa, sa + 4, keep);
+          else
+            mma_bf16<0>(tmem_base, da, db, idesc, keep);
+        }
+        tc_commit(bar_empty + 8 * s);
+      }
+      if (ok) tc_commit(bar_acc);
+    }
+  } else {
+    // accumulator -> shared memory as [token][row] (the stages are free: all
+    // products that read them are done)
+    float* acc = reinterpret_cast<float*>(smem);
+    if (__all_sync(0xFFFFFFFFu, mbar_wait(bar_acc, 0, args.status, abort_flag))) {
+      tc_fence_after();
+      const int row = (warp & 3) * 32 + lane;
+      const uint32_t tb = tmem_base + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+#pragma unroll
+      for (int c = (warp >> 2) * 16; c < BN; c += 32) {
+        float v[16];
+        tmem_ld16(tb + c, v);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[(c + i) * 128 + row] = v[i];
+      }
+      tc_fence_before();
+    }
+  }
+  if (S > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+
+  // A thread adds up four rows (gated: four gate rows and the four up rows
+  // beside them) of U tokens at a time, so that all its reads of the other
+  // CTAs are in flight together (one such read takes about 500 clocks).
+  constexpr int LANES = GATED ? 16 : 32, GROUPS = 256 / LANES, U = GATED ? 2 : 4;
+  const int share = (BN + S - 1) / S;
+  const int last = min(min(BN, (rank + 1) * share), args.tokens - tt * BN);
+  const int sub = threadIdx.x % LANES;
+  const int col = wt * (GATED ? 64 : 128) + sub * 4;
+  int t0 = rank * share + static_cast<int>(threadIdx.x) / LANES;
+  if (warp >= 8 || col >= args.rows) t0 = last;
+  for (; t0 < last; t0 += U * GROUPS) {
+    const uint32_t base = smem_u32(smem) + sub * 16;
+    float4 v[U], u[GATED ? U : 1];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (GATED) u[k] = v[k];
+    }
+    if (S == 1) {
+#pragma unroll
+      for (int k = 0; k < U; ++k) {  // past the end: the last token again, not stored
+        const uint32_t at = base + min(t0 + k * GROUPS, BN - 1) * 512;
+        v[k] = ld_shared_f4(at);
+        if (GATED) u[k] = ld_shared_f4(at + 256);
+      }
+    } else {
+#pragma unroll 4
+      for (int p = 0; p < S; ++p) {
+        const uint32_t from = map_rank(base, p);
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+          const uint32_t at = from + min(t0 + k * GROUPS, BN - 1) * 512;
+          add4(v[k], ld_cluster_f4(at));
+          if (GATED) add4(u[k], ld_cluster_f4(at + 256));
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int t = t0 + k * GROUPS;
+      const int64_t token = static_cast<int64_t>(tt) * BN + t;
+      if (t < last) {
+        const int64_t at = token * args.rows + col;
+        if (GATED) {
+          put4(static_cast<bf16*>(args.out) + at, gate4(v[k], u[k], args.act));
+          const int64_t o = at + token * args.rows;
+          if (args.save.f32) {
+            put4(args.save.f32 + o, v[k]);
+            put4(args.save.f32 + o + args.rows, u[k]);
+          } else if (args.save.b16) {
+            put4(args.save.b16 + o, v[k]);
+            put4(args.save.b16 + o + args.rows, u[k]);
+          }
+        } else if (OUT == FF_F32) {
+          put4(static_cast<float*>(args.out) + at, v[k]);
+        } else {
+          put4(static_cast<bf16*>(args.out) + at, v[k]);
+        }
+      }
+    }
+  }
+  if (S > 1) cluster_sync();  // the others may still be reading this CTA's copy
+  if (*abort_flag) {
+    // give bulk copies already in flight time to land before the CTA ends
+    for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+  }
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, TMEM_COLS);
+  }
+}
+
+template <int F8, int W_MN, int BN, int OUT>
+cudaError_t launch(const CUtensorMap (&tm)[4], const NarrowArgs& a, int stages, int S, int tiles,
+                   cudaStream_t s) {
+  static bool ready[64] = {};
+  if (cudaError_t e = ff_all_smem(k_narrow<F8, W_MN, BN, OUT>, ready)) return e;
+  count_launch();
+  return ff_launch(k_narrow<F8, W_MN, BN, OUT>, static_cast<int64_t>(tiles) * S, THREADS,
+                   stages * (W_BYTES + BN * 128 + (F8 ? SCALES : 0)) + 1024 + 512, S, s, tm[0],
+                   tm[1], tm[2], tm[3], a, stages, S);
+}
+
+}  // namespace
+
+bool ff_narrow_product(const FfProduct& p, cudaStream_t s, cudaError_t* err) {
+  // here the activations are p.a [tokens, K] and the weights p.b
+  const bool gated = p.out_kind == FF_GATED;
+  if (p.a_mn || (p.b_mn && (p.f8 || gated)) || p.save.q) return false;
+  const int K = p.f8 ? p.K / 2 : p.K;
+  const int kblocks = (K + 63) / 64;
+  const FfNarrowPlan plan = ff_narrow_plan(p.M, gated ? 2 * p.N : p.N, kblocks);
+  const int bn = plan.bn;
+  CUtensorMap tm[4];
+  memset(tm, 0, sizeof(tm));
+  if (!(p.b_mn ? make_tmap_bf16(&tm[0], p.b, p.N, K, 2ull * p.N, 64, 64)
+               : make_tmap_bf16(&tm[0], p.b, K, gated ? 2 * p.N : p.N, 2ull * K, 64, 64)) ||
+      !make_tmap_bf16(&tm[1], p.a, K, p.M, 2ull * K, 64, bn))
+    return false;
+  NarrowArgs a;
+  memset(&a, 0, sizeof(a));
+  a.tokens = p.M;
+  a.rows = p.N;
+  a.kblocks = kblocks;
+  a.token_tiles = (p.M + bn - 1) / bn;
+  a.act = p.act;
+  a.fresh = p.fresh;
+  a.out = p.out;
+  a.save = p.save;
+  a.status = p.status;
+  if (p.f8) {
+    a.k_tiles = (p.K + F8_TILE_COLS - 1) / F8_TILE_COLS;
+    if (!make_tmap_u32(&tm[2], p.b_scales, 128,
+                       static_cast<uint64_t>((p.N + 127) / 128) * a.k_tiles, 128, 1) ||
+        !make_tmap_u32(&tm[3], p.a_scales, 128,
+                       static_cast<uint64_t>((p.M + 127) / 128) * a.k_tiles, 128, 1))
+      return false;
+    a.idesc = idesc_f8(128, bn, p.b_e5m2, p.a_e5m2);
+  } else {
+    a.idesc = idesc_bf16(128, bn, p.b_mn, 0);
+  }
+  a.per = (a.kblocks + plan.split - 1) / plan.split;
+  const int tiles = plan.tiles, S = plan.split;
+  const int stage = W_BYTES + bn * 128 + (p.f8 ? SCALES : 0);
+  // up to 64 tokens half an SM's shared memory, so that two CTAs are resident,
+  // of this launch or of the next one
+  int stages = ((bn <= 64 ? 112 : 224) * 1024 - 1536) / stage;
+  if (stages > a.per && a.per * stage >= bn * 512) stages = a.per;
+  // the accumulator's copy (512 bytes per token) reuses the stages
+  while (stages * stage < bn * 512) ++stages;
+#define ALX_NARROW(F8_, MN_, OUT_, BN_)                                              \
+  if (p.f8 == F8_ && p.b_mn == MN_ && p.out_kind == OUT_ && bn == BN_) {              \
+    *err = launch<F8_, MN_, BN_, OUT_>(tm, a, stages, S, tiles, s);                   \
+    return true;                                                                      \
+  }
+#define ALX_NARROW_ALL(F8_, MN_, OUT_)                                                \
+  ALX_NARROW(F8_, MN_, OUT_, 16) ALX_NARROW(F8_, MN_, OUT_, 32)                       \
+  ALX_NARROW(F8_, MN_, OUT_, 64) ALX_NARROW(F8_, MN_, OUT_, 128)
+  ALX_NARROW_ALL(0, 0, FF_GATED)
+  ALX_NARROW_ALL(0, 0, FF_F32)
+  ALX_NARROW_ALL(0, 1, FF_BF16)
+  ALX_NARROW_ALL(1, 0, FF_BF16)
+  ALX_NARROW_ALL(1, 0, FF_F32)
+#undef ALX_NARROW_ALL
+#undef ALX_NARROW
+  return false;
+}
+
+// What a narrow product costs, in ns, fitted to a B200 (back to back, rows 512
+// to 18432, K 512 to 18432 elements, 1 to 2048 tokens): 5.5 us of first loads
+// and epilogue, 1 us and 16 ns per token of the tile more to join a cluster;
+// then the slowest of reading the weights (6.3 TB/s, 5.5 with one CTA per SM),
+// moving all operands into the SMs (12 TB/s), and the steps of K that one SM
+// walks (0.27 us each); a second wave of CTAs starts over (4.5 us).  Over 230
+// sizes the kernel that this and ff_pair_ns choose takes 1% more than the
+// faster of the two in the mean.
+// Clusters of more than four lost to four at every size measured (they leave
+// SMs of a GPC over and join more slowly), so S <= 4.  Two CTAs per SM have
+// 112 KB each: four stages up to 64 tokens but three at 128, which is too few
+// to cover a load's latency, so that split is not made there.
+FfNarrowPlan ff_narrow_plan(int tokens, int rows, int kblocks) {
+  const double sms = ff_num_sms();
+  const int bn = tokens <= 16 ? 16 : (tokens <= 32 ? 32 : (tokens <= 64 ? 64 : 128));
+  FfNarrowPlan p;
+  p.bn = bn;
+  p.tiles = ((rows + 127) / 128) * ((tokens + bn - 1) / bn);
+  p.split = 1;
+  p.ns = 0;
+  const double weights = 128.0 * rows * kblocks;
+  const double moved = 128.0 * (128 + bn) * p.tiles * kblocks;
+  for (int S = 1; S <= 4 && S <= kblocks; ++S) {
+    const int per = (kblocks + S - 1) / S;
+    if ((kblocks + per - 1) / per != S) continue;  // a CTA would have nothing to do
+    const double ctas = static_cast<double>(p.tiles) * S;
+    const bool two = bn <= 64 && ctas > sms;
+    if (S > 1 && ctas > (two ? 2 : 1) * (S > 2 ? 0.97 : 1.0) * sms) break;
+    double waves = ctas / sms;
+    if (waves < 1) waves = 1;
+    if (!two) waves = static_cast<double>(static_cast<int64_t>(waves + 0.999));
+    double t = weights / (ctas < 1.3 * sms ? 5500 : 6300);
+    if (moved / 12000 > t) t = moved / 12000;
+    if (waves * per * 270 > t) t = waves * per * 270;
+    t += 5500 + (S > 1 ? 1000 + 16 * bn : 0) + (two ? 0 : 4500 * (waves - 1));
+    if (p.ns == 0 || t < p.ns) {
+      p.ns = t;
+      p.split = S;
+    }
+  }
+  return p;
+}
+
+}  // namespace alx

@@ -7,7 +7,6 @@
 #include "f8.cuh"
 #include "ff.h"
 #include "ff_gemm.h"
-#include "ff_pair.h"
 
 using namespace alx;
 
@@ -34,11 +33,24 @@ bool gated_dims(int B, int In, int F, int step) {
   return B >= 1 && In >= 1 && F >= 1 && In % step == 0 && F % step == 0;
 }
 
+// The narrow kernel reads every weight tile once per 128 tokens and splits the
+// reduction, the pairs' one has a quarter of the operand traffic per product:
+// the one whose expected time is shorter.  Measured (us, narrow / pairs): gated
+// block 4096 -> 9216 with 1 token 27 / 43, 128 tokens 32 / 33, 384 tokens 73 /
+// 53; 8-bit product 9216 -> 4096 with 128 tokens 15 / 32, 512 tokens 29 / 32.
+bool runs_narrow(const FfProduct& p) {
+  if (p.a_mn) return false;
+  const int rows = p.out_kind == FF_GATED ? 2 * p.N : p.N;
+  const int kblocks = ((p.f8 ? p.K : 2 * p.K) + 127) / 128;
+  return ff_narrow_plan(p.M, rows, kblocks).ns < ff_pair_ns(p.M, rows, kblocks);
+}
+
 alexnet_status product(const FfProduct& p, cudaStream_t s) {
   if (static_cast<int64_t>((p.M + 127) / 128) * ((p.N + 127) / 128) > 0x7FFFFFFF)
     return ALEXNET_ERR_UNSUPPORTED;
   cudaError_t e = cudaSuccess;
-  if (!ff_pair_product(p, s, &e)) return ALEXNET_ERR_UNSUPPORTED;
+  if (!(runs_narrow(p) ? ff_narrow_product(p, s, &e) : ff_pair_product(p, s, &e)))
+    return ALEXNET_ERR_UNSUPPORTED;
   return done(e);
 }
 
@@ -140,7 +152,7 @@ alexnet_status alexnet_op_fc_f8_fwd(const void* x, const uint8_t* xs, int x_fmt,
 
 size_t alexnet_gated_workspace_bytes(int B, int In, int F) {
   if (!gated_dims(B, In, F, 8) || In > MAX_DIM || F > MAX_DIM) return 0;
-  return 256 + up256(4ull * B * F) + up256(2ull * B * In);
+  return 256 + up256(8ull * B * F) + up256(2ull * B * In);
 }
 
 }  // extern "C"
@@ -171,6 +183,16 @@ alexnet_status gated_fwd(const void* x, int B, int In, const void* w, int F, int
   p.act = act;
   p.save = save;
   p.fresh = 1;
+  if (save.q && runs_narrow(p)) {
+    // the narrow kernel's tiles hold 64 columns, half a block of the codes:
+    // the projections go to the workspace and one kernel gates and codes them
+    float* z = reinterpret_cast<float*>(U8(ws) + 256);
+    FfProduct both = bf16_product(x, 0, w, 0, B, 2 * F, In, z, static_cast<int*>(ws));
+    both.out_kind = FF_F32;
+    both.fresh = 1;
+    if (alexnet_status e = product(both, s)) return e;
+    return done(launch_gate_fwd(z, B, F, act, B16(h), save, s));
+  }
   return product(p, s);
 }
 
@@ -178,9 +200,8 @@ alexnet_status gated_bwd(const void* dh, const void* x, const GateSave& save, in
                          const void* w, int F, int act, void* dx, void* dw, void* ws,
                          cudaStream_t s) {
   bf16* dz = reinterpret_cast<bf16*>(U8(ws) + 256);
-  cudaMemsetAsync(ws, 0, 4, s);
-  if (cudaError_t e = launch_gate_bwd(B16(dh), save, B, F, act, dz, s)) return done(e);
   int* status = static_cast<int*>(ws);
+  if (cudaError_t e = launch_gate_bwd(B16(dh), save, B, F, act, dz, status, s)) return done(e);
   if (dx)
     if (alexnet_status e = product(bf16_product(dz, 0, w, 1, B, In, 2 * F, dx, status), s))
       return e;
@@ -233,7 +254,7 @@ alexnet_status alexnet_op_gated_bwd_ckpt8(const void* dh, const void* xq, const 
     return ALEXNET_ERR_INVALID_ARG;
   if (In > MAX_DIM || F > MAX_DIM) return ALEXNET_ERR_UNSUPPORTED;
   if (!ws || ws_bytes < alexnet_gated_workspace_bytes(B, In, F)) return ALEXNET_ERR_INVALID_ARG;
-  bf16* xb = reinterpret_cast<bf16*>(U8(ws) + 256 + up256(4ull * B * F));
+  bf16* xb = reinterpret_cast<bf16*>(U8(ws) + 256 + up256(8ull * B * F));
   if (dw)
     if (cudaError_t e = launch_f8_dequant(U8(xq), xs, B, In, ALEXNET_E4M3, xb, cu(stream)))
       return done(e);

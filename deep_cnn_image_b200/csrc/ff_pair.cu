@@ -27,7 +27,6 @@
 
 #include "f8.cuh"
 #include "ff_gemm.h"
-#include "ff_pair.h"
 #include "gate.cuh"
 #include "gemm.h"
 #include "kernels.h"
@@ -195,7 +194,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   const uint32_t rank = cluster_rank();
 
   if (threadIdx.x == 0) {
-    if (args.fresh && blockIdx.x == 0) *args.status = 0;
     for (int s = 0; s < stages; ++s) {
       mbar_init(bar_full + 8 * s, 1);
       mbar_init(bar_empty + 8 * s, 1);
@@ -214,6 +212,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  grid_dep_launch();
+  grid_dep_wait();
+  if (args.fresh && blockIdx.x == 0 && threadIdx.x == 0) *args.status = 0;
 
   const int total = args.m_tiles * args.n_tiles;
   const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
@@ -341,7 +342,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       int m, n;
       tile_at(args, t, m, n);
       const uint32_t acc = count & 1;
-      if (!mbar_wait(bar_acc_full + 8 * acc, (count >> 1) & 1, args.status, abort_flag)) break;
+      // the whole warp goes on or none of it does
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait(bar_acc_full + 8 * acc, (count >> 1) & 1, args.status,
+                                             abort_flag)))
+        break;
       tc_fence_after();
       const int64_t row = static_cast<int64_t>(m) * 256 + rank * 128 + quarter * 32 + lane;
       const bool live = row < args.M;
@@ -442,21 +446,23 @@ template <int F8, int A_MN, int B_MN, int OUT>
 cudaError_t launch(const CUtensorMap (&tm)[4], const PairArgs& a, int stages, int smem, int grid,
                    cudaStream_t s) {
   static bool ready[64] = {};
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev < 0 || dev >= 64 || !ready[dev]) {
-    if (cudaError_t e = cudaFuncSetAttribute(k_pair<F8, A_MN, B_MN, OUT>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             227 * 1024))
-      return e;
-    if (dev >= 0 && dev < 64) ready[dev] = true;
-  }
+  if (cudaError_t e = ff_all_smem(k_pair<F8, A_MN, B_MN, OUT>, ready)) return e;
   count_launch();
-  k_pair<F8, A_MN, B_MN, OUT><<<grid, THREADS, smem, s>>>(tm[0], tm[1], tm[2], tm[3], a, stages);
-  return cudaGetLastError();
+  return ff_launch(k_pair<F8, A_MN, B_MN, OUT>, grid, THREADS, smem, 0, s, tm[0], tm[1], tm[2],
+                   tm[3], a, stages);
 }
 
 }  // namespace
+
+// Fitted like ff_narrow_plan: 7 us, then 0.34 us per step of K and tile on the
+// busiest pair, or the weights at 5.5 TB/s.
+double ff_pair_ns(int tokens, int rows, int kblocks) {
+  const int64_t pairs = ff_num_sms() / 2;
+  const int64_t tiles = static_cast<int64_t>((tokens + 255) / 256) * ((rows + 255) / 256);
+  const double steps = static_cast<double>((tiles + pairs - 1) / pairs) * kblocks * 340;
+  const double weights = 128.0 * rows * kblocks / 5500;
+  return 7000 + (steps > weights ? steps : weights);
+}
 
 bool ff_pair_product(const FfProduct& p, cudaStream_t s, cudaError_t* err) {
   CUtensorMap tm[4];

@@ -17,6 +17,8 @@ namespace {
 __global__ void __launch_bounds__(256)
     k_gate_fwd(const float* __restrict__ z, int B, int F, int act, bf16* __restrict__ h,
                const GateSave save) {
+  grid_dep_launch();
+  grid_dep_wait();
   bf16* gu = save.b16;
   uint8_t *guq = save.q, *gus = save.qs;
   const int blocks = (F + F8_BLOCK - 1) / F8_BLOCK;
@@ -86,7 +88,10 @@ __global__ void __launch_bounds__(256)
 template <int KIND>
 __global__ void __launch_bounds__(256)
     k_gate_bwd(const bf16* __restrict__ dh, const GateSave save, int B, int F, int act,
-               bf16* __restrict__ dz) {
+               bf16* __restrict__ dz, int* status) {
+  grid_dep_launch();
+  grid_dep_wait();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *status = 0;
   const bf16* __restrict__ gu = save.b16;
   const uint8_t *__restrict__ guq = save.q, *__restrict__ gus = save.qs;
   const int vecs = F >> 3;
@@ -150,22 +155,16 @@ int grid_for(int64_t blocks) {
 cudaError_t launch_gate_fwd(const float* z, int B, int F, int act, bf16* h, const GateSave& save,
                             cudaStream_t s) {
   const int64_t blocks = static_cast<int64_t>(B) * ((F + F8_BLOCK - 1) / F8_BLOCK);
-  k_gate_fwd<<<grid_for((blocks + 15) / 16), 256, 0, s>>>(z, B, F, act, h, save);
   count_launch();
-  return cudaGetLastError();
+  return ff_launch(k_gate_fwd, grid_for((blocks + 15) / 16), 256, 0, 0, s, z, B, F, act, h, save);
 }
 
 cudaError_t launch_gate_bwd(const bf16* dh, const GateSave& save, int B, int F, int act, bf16* dz,
-                            cudaStream_t s) {
+                            int* status, cudaStream_t s) {
   const int grid = grid_for((static_cast<int64_t>(B) * (F >> 3) + 255) / 256);
-  if (save.b16)
-    k_gate_bwd<0><<<grid, 256, 0, s>>>(dh, save, B, F, act, dz);
-  else if (save.q)
-    k_gate_bwd<1><<<grid, 256, 0, s>>>(dh, save, B, F, act, dz);
-  else
-    k_gate_bwd<2><<<grid, 256, 0, s>>>(dh, save, B, F, act, dz);
   count_launch();
-  return cudaGetLastError();
+  return ff_launch(save.b16 ? k_gate_bwd<0> : (save.q ? k_gate_bwd<1> : k_gate_bwd<2>), grid, 256,
+                   0, 0, s, dh, save, B, F, act, dz, status);
 }
 
 }  // namespace alx

@@ -120,6 +120,16 @@ struct RingPos {
   }
 };
 
+// ---------------------------------------------------------------- dependent launches
+// Allow the next kernel of the stream to be launched (once every block of
+// this grid has called it), and wait for the kernels before this one.
+__device__ __forceinline__ void grid_dep_launch() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void grid_dep_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // ---------------------------------------------------------------- fences
 __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");

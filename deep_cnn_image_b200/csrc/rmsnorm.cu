@@ -77,6 +77,8 @@ __global__ void __launch_bounds__(G > 32 ? G : 256)
                   const float* __restrict__ gamma, int64_t rows, int cols, float eps,
                   bf16* sum, bf16* y, float* rstd, uint8_t* q, uint8_t* scales) {
   __shared__ float red[32];
+  grid_dep_launch();
+  grid_dep_wait();
   const int t = G > 32 ? threadIdx.x : (threadIdx.x & 31);
   const int64_t row =
       G > 32 ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
@@ -154,6 +156,8 @@ __global__ void __launch_bounds__(G > 32 ? G : 256)
                   const float* __restrict__ gamma, const float* __restrict__ rstd, int64_t rows,
                   int cols, bf16* dx, float* __restrict__ parts) {
   __shared__ float red[2][32];
+  grid_dep_launch();
+  grid_dep_wait();
   const int t = G > 32 ? threadIdx.x : (threadIdx.x & 31);
   const int64_t first =
       G > 32 ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
@@ -221,6 +225,8 @@ __global__ void __launch_bounds__(G > 32 ? G : 256)
 __global__ void __launch_bounds__(512)
     k_sum_parts(const float* __restrict__ parts, int n, int cols, float* __restrict__ out) {
   __shared__ float red[16][33];
+  grid_dep_launch();
+  grid_dep_wait();
   const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float a = 0.f;
@@ -239,6 +245,8 @@ __global__ void __launch_bounds__(512)
 __global__ void __launch_bounds__(256)
     k_f8_quant(const bf16* __restrict__ x, int64_t rows, int cols, int e5m2,
                uint8_t* __restrict__ q, uint8_t* __restrict__ scales) {
+  grid_dep_launch();
+  grid_dep_wait();
   const int blocks = (cols + F8_BLOCK - 1) / F8_BLOCK;
   const int col_tiles = (cols + F8_TILE_COLS - 1) / F8_TILE_COLS;
   const int64_t total = rows * blocks;
@@ -262,6 +270,8 @@ __global__ void __launch_bounds__(256)
 __global__ void __launch_bounds__(256)
     k_f8_dequant(const uint8_t* __restrict__ q, const uint8_t* __restrict__ scales, int64_t rows,
                  int cols, int e5m2, bf16* __restrict__ x) {
+  grid_dep_launch();
+  grid_dep_wait();
   const int vecs = cols >> 4;
   const int col_tiles = (cols + F8_TILE_COLS - 1) / F8_TILE_COLS;
   const int64_t total = rows * vecs;
@@ -316,7 +326,7 @@ int ff_num_sms() {
 // Threads per row by its width: a warp up to 1024 columns (no block
 // barrier, eight rows per block), 256 threads up to 16384, 1024 beyond.
 #define ALX_ROWS(G_, NV_, KERNEL, GRID, ...) \
-  KERNEL<G_, NV_><<<GRID, G_ > 32 ? G_ : 256, 0, s>>>(__VA_ARGS__)
+  e = ff_launch(KERNEL<G_, NV_>, GRID, G_ > 32 ? G_ : 256, 0, 0, s, __VA_ARGS__)
 #define ALX_ROWS_BY_WIDTH(KERNEL, WARP_GRID, ROW_GRID, ...)                       \
   if (cols <= 256) ALX_ROWS(32, 1, KERNEL, WARP_GRID, __VA_ARGS__);               \
   else if (cols <= 512) ALX_ROWS(32, 2, KERNEL, WARP_GRID, __VA_ARGS__);          \
@@ -331,11 +341,12 @@ int ff_num_sms() {
 cudaError_t launch_rmsnorm_fwd(const bf16* x, const bf16* res, const float* gamma, int64_t rows,
                                int cols, float eps, bf16* sum, bf16* y, float* rstd, uint8_t* q,
                                uint8_t* scales, cudaStream_t s) {
-  const unsigned wg = static_cast<unsigned>((rows + 7) / 8), rg = static_cast<unsigned>(rows);
+  const int64_t wg = (rows + 7) / 8, rg = rows;
+  cudaError_t e = cudaSuccess;
   ALX_ROWS_BY_WIDTH(k_rmsnorm_fwd, wg, rg, x, res, gamma, rows, cols, eps, sum, y, rstd, q,
                     scales);
   count_launch();
-  return cudaGetLastError();
+  return e;
 }
 
 int rmsnorm_bwd_parts(int64_t rows, int cols) {
@@ -346,31 +357,32 @@ cudaError_t launch_rmsnorm_bwd(const bf16* dy, const bf16* dsum, const bf16* sum
                                const float* gamma, const float* rstd, int64_t rows, int cols,
                                bf16* dx, float* dgamma, float* parts, cudaStream_t s) {
   const int grid = bwd_grid(rows, cols);
+  cudaError_t e = cudaSuccess;
   ALX_ROWS_BY_WIDTH(k_rmsnorm_bwd, grid, grid, dy, dsum, sum, gamma, rstd, rows, cols, dx,
-                    dgamma ? parts : nullptr);
+                    dgamma ? parts : static_cast<float*>(nullptr));
   count_launch();
-  if (dgamma) {
-    k_sum_parts<<<(cols + 31) / 32, 512, 0, s>>>(parts, rmsnorm_bwd_parts(rows, cols), cols,
-                                                 dgamma);
+  if (dgamma && e == cudaSuccess) {
+    e = ff_launch(k_sum_parts, (cols + 31) / 32, 512, 0, 0, s, parts,
+                  rmsnorm_bwd_parts(rows, cols), cols, dgamma);
     count_launch();
   }
-  return cudaGetLastError();
+  return e;
 }
 
 cudaError_t launch_f8_quant(const bf16* x, int64_t rows, int cols, int e5m2, uint8_t* q,
                             uint8_t* scales, cudaStream_t s) {
   const int64_t blocks = rows * ((cols + F8_BLOCK - 1) / F8_BLOCK);
-  k_f8_quant<<<grid_for((blocks + 15) / 16), 256, 0, s>>>(x, rows, cols, e5m2, q, scales);
   count_launch();
-  return cudaGetLastError();
+  return ff_launch(k_f8_quant, grid_for((blocks + 15) / 16), 256, 0, 0, s, x, rows, cols, e5m2, q,
+                   scales);
 }
 
 cudaError_t launch_f8_dequant(const uint8_t* q, const uint8_t* scales, int64_t rows, int cols,
                               int e5m2, bf16* x, cudaStream_t s) {
   const int64_t vecs = rows * (cols >> 4);
-  k_f8_dequant<<<grid_for((vecs + 255) / 256), 256, 0, s>>>(q, scales, rows, cols, e5m2, x);
   count_launch();
-  return cudaGetLastError();
+  return ff_launch(k_f8_dequant, grid_for((vecs + 255) / 256), 256, 0, 0, s, q, scales, rows, cols,
+                   e5m2, x);
 }
 
 }  // namespace alx
