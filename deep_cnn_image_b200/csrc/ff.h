@@ -38,15 +38,16 @@ cudaError_t ff_launch(void (*kernel)(P...), int64_t grid, int block, int smem, i
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
 }
 
-// Lets a kernel use all of an SM's shared memory; once per kernel and device.
+// Lets a kernel use all of an SM's shared memory but what it declares
+// statically (`fixed` bytes at most); once per kernel and device.
 template <typename K>
-cudaError_t ff_all_smem(K kernel, bool (&ready)[64]) {
+cudaError_t ff_all_smem(K kernel, bool (&ready)[64], int fixed = 0) {
   int dev = 0;
   cudaGetDevice(&dev);
   const bool known = dev >= 0 && dev < 64;
   if (known && ready[dev]) return cudaSuccess;
   const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - fixed);
   if (known && e == cudaSuccess) ready[dev] = true;
   return e;
 }
@@ -60,7 +61,7 @@ cudaError_t launch_rmsnorm_fwd(const bf16* x, const bf16* res, const float* gamm
 int rmsnorm_bwd_parts(int64_t rows, int cols);
 cudaError_t launch_rmsnorm_bwd(const bf16* dy, const bf16* dsum, const bf16* sum,
                                const float* gamma, const float* rstd, int64_t rows, int cols,
-                               bf16* dx, float* dgamma, float* parts, cudaStream_t s);
+                               bf16* dx, float* dgamma, float* parts, int* status, cudaStream_t s);
 cudaError_t launch_f8_quant(const bf16* x, int64_t rows, int cols, int e5m2, uint8_t* q,
                             uint8_t* scales, cudaStream_t s);
 cudaError_t launch_f8_dequant(const uint8_t* q, const uint8_t* scales, int64_t rows, int cols,

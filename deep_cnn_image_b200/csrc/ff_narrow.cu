@@ -30,6 +30,9 @@ namespace alx {
 namespace {
 
 constexpr int THREADS = 320;
+// steps of K whose weights are prefetched: the gated block 4096 -> 9216 with one
+// token 26.8 -> 25.8 us; 8 give 25.6 there but cost 0.3 us at 128 tokens
+constexpr int AHEAD = 4;
 constexpr int W_BYTES = 128 * 128;      // weight rows of a stage
 constexpr int BOX_BYTES = 64 * 128;     // one of its two boxes
 constexpr int SCALES = 2 * F8_TILE_BYTES;
@@ -98,6 +101,9 @@ __global__ void __launch_bounds__(THREADS)
   const int tt = tile % args.token_tiles, wt = tile / args.token_tiles;
   const int kb0 = rank * args.per;
   const int kb1 = min(args.kblocks, kb0 + args.per);
+  // first rows of the tile's two boxes of weights
+  const int w0 = GATED ? wt * 64 : wt * 128;
+  const int w1 = GATED ? args.rows + w0 : w0 + 64;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
@@ -117,6 +123,7 @@ __global__ void __launch_bounds__(THREADS)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  grid_dep_launch();
   if (warp == 8 && lane == 0) {
     tma_prefetch_desc(&tmW);
     tma_prefetch_desc(&tmX);
@@ -124,16 +131,24 @@ __global__ void __launch_bounds__(THREADS)
       tma_prefetch_desc(&tmSW);
       tma_prefetch_desc(&tmSX);
     }
+    // While the kernel before this one ends, the first weights come to L2.
+    // That is safe even where that kernel writes them: L2 holds its writes.
+    for (int kb = kb0; kb < min(kb1, kb0 + AHEAD); ++kb) {
+      if (W_MN) {
+        tma_prefetch_2d(&tmW, w0, kb * 64);
+        tma_prefetch_2d(&tmW, w1, kb * 64);
+      } else {
+        tma_prefetch_2d(&tmW, kb * 64, w0);
+        tma_prefetch_2d(&tmW, kb * 64, w1);
+      }
+    }
   }
-  grid_dep_launch();
   grid_dep_wait();
   if (args.fresh && blockIdx.x == 0 && threadIdx.x == 0) *args.status = 0;
 
   if (warp == 8) {
     if (lane == 0) {
       RingPos r;
-      const int w0 = GATED ? wt * 64 : wt * 128;
-      const int w1 = GATED ? args.rows + w0 : w0 + 64;
       for (int kb = kb0; kb < kb1; ++kb, r.next(stages)) {
         const uint32_t s = r.slot;
         if (!mbar_wait(bar_empty + 8 * s, r.phase ^ 1, args.status, abort_flag)) break;
@@ -370,9 +385,10 @@ bool ff_narrow_product(const FfProduct& p, cudaStream_t s, cudaError_t* err) {
 // What a narrow product costs, in ns, fitted to a B200 (back to back, rows 512
 // to 18432, K 512 to 18432 elements, 1 to 2048 tokens): 5.5 us of first loads
 // and epilogue, 1 us and 16 ns per token of the tile more to join a cluster;
-// then the slowest of reading the weights (6.3 TB/s, 5.5 with one CTA per SM),
-// moving all operands into the SMs (12 TB/s), and the steps of K that one SM
-// walks (0.27 us each); a second wave of CTAs starts over (4.5 us).  Over 230
+// then the slowest of reading the weights (6.3 TB/s, 5.5 with about one CTA per
+// SM, at most 45 GB/s per CTA), moving all operands into the SMs (12 TB/s), and
+// the steps of K that one SM walks (0.27 us each); a second wave of CTAs starts
+// over (4.5 us).  Over 230
 // sizes the kernel that this and ff_pair_ns choose takes 1% more than the
 // faster of the two in the mean.
 // Clusters of more than four lost to four at every size measured (they leave
@@ -398,11 +414,13 @@ FfNarrowPlan ff_narrow_plan(int tokens, int rows, int kblocks) {
     double waves = ctas / sms;
     if (waves < 1) waves = 1;
     if (!two) waves = static_cast<double>(static_cast<int64_t>(waves + 0.999));
-    double t = weights / (ctas < 1.3 * sms ? 5500 : 6300);
+    double rate = ctas < 1.3 * sms ? 5500 : 6300;  // bytes per ns
+    if (ctas * 45 < rate) rate = ctas * 45;
+    double t = weights / rate;
     if (moved / 12000 > t) t = moved / 12000;
     if (waves * per * 270 > t) t = waves * per * 270;
     t += 5500 + (S > 1 ? 1000 + 16 * bn : 0) + (two ? 0 : 4500 * (waves - 1));
-    if (p.ns == 0 || t < p.ns) {
+    if (p.ns == 0 || t <= p.ns) {
       p.ns = t;
       p.split = S;
     }

@@ -119,7 +119,8 @@ alexnet_status alexnet_op_rmsnorm_bwd(const void* dy, const void* dsum, const vo
   if (cols > RMSNORM_MAX_COLS || rows > 0x7FFFFFFF) return ALEXNET_ERR_UNSUPPORTED;
   if (!ws || ws_bytes < alexnet_rmsnorm_workspace_bytes(rows, cols)) return ALEXNET_ERR_INVALID_ARG;
   return done(launch_rmsnorm_bwd(B16(dy), B16(dsum), B16(s), gamma, rstd, rows, cols, B16(dx),
-                                 dgamma, reinterpret_cast<float*>(U8(ws) + 256), cu(stream)));
+                                 dgamma, reinterpret_cast<float*>(U8(ws) + 256), static_cast<int*>(ws),
+                                 cu(stream)));
 }
 
 size_t alexnet_fc_f8_workspace_bytes(int B, int In, int Out) {

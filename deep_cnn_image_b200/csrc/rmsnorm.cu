@@ -12,20 +12,20 @@ namespace alx {
 
 namespace {
 
-// Sum over the G threads (32 or a whole block of G) that share a row; the
-// order is fixed, so results are reproducible.  `red` holds G / 32 floats.
-template <int G>
+// Sum over the threads that share a row: a warp, or (BLOCK) a whole block of
+// whole warps; the order is fixed, so results are reproducible.  `red` holds
+// 32 floats.
+template <bool BLOCK>
 __device__ __forceinline__ float row_sum(float v, float* red) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  if (G > 32) {
+  if (BLOCK) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (lane == 0) red[warp] = v;
     __syncthreads();
-    v = lane < G / 32 ? red[lane] : 0.f;
+    v = lane < static_cast<int>(blockDim.x >> 5) ? red[lane] : 0.f;
 #pragma unroll
-    for (int o = G / 64; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    v = __shfl_sync(0xFFFFFFFFu, v, 0);
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   }
   return v;
 }
@@ -67,22 +67,25 @@ __device__ __forceinline__ uint2 codes8(const float (&f)[8], float inv, int e5m2
 }
 
 // y = s * rstd * gamma with s = bf16(x + res), rstd = 1/sqrt(mean(s^2) + eps).
-// One pass over the row: G threads hold it in registers as bf16 (NV vectors of
-// 8 columns each, thread t the vectors t, t + G, ...), so the rounded s is
-// also what the statistic and the gradient see.  16 neighbouring lanes hold
-// one 128-column block of the 8-bit output.
-template <int G, int NV>
-__global__ void __launch_bounds__(G > 32 ? G : 256)
-    k_rmsnorm_fwd(const bf16* x, const bf16* res,
-                  const float* __restrict__ gamma, int64_t rows, int cols, float eps,
-                  bf16* sum, bf16* y, float* rstd, uint8_t* q, uint8_t* scales) {
+// One pass over the row: G threads (a warp, eight rows per block; or BLOCK: a
+// block) hold it in registers as bf16, NV vectors of 8 columns each (thread t
+// the vectors t, t + G, ...), so the rounded s is also what the statistic and
+// the gradient see.  16 neighbouring lanes hold one 128-column block of the
+// 8-bit output.  Bound by its bytes (x, res, s, codes: 7 per column): 6.1 TB/s,
+// 0.93 of a copy, at 8192 x 4096.
+template <int NV, bool BLOCK>
+__global__ void __launch_bounds__(NV > 4 ? 1024 : 512)
+    k_rmsnorm_fwd(const bf16* x, const bf16* res, const float* __restrict__ gamma, int64_t rows,
+                  int cols, float eps, bf16* sum, bf16* y, float* rstd, uint8_t* q,
+                  uint8_t* scales) {
   __shared__ float red[32];
   grid_dep_launch();
   grid_dep_wait();
-  const int t = G > 32 ? threadIdx.x : (threadIdx.x & 31);
+  const int G = BLOCK ? blockDim.x : 32;
+  const int t = BLOCK ? threadIdx.x : (threadIdx.x & 31);
   const int64_t row =
-      G > 32 ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  if (row >= rows) return;  // whole warps of a G = 32 block only
+      BLOCK ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (row >= rows) return;  // whole warps of a block of eight rows only
   const int nvec = cols >> 3;
   const bf16* xr = x + row * cols;
   uint4 v[NV];
@@ -115,7 +118,7 @@ __global__ void __launch_bounds__(G > 32 ? G : 256)
 #pragma unroll
     for (int i = 0; i < 8; ++i) ss += a[i] * a[i];
   }
-  ss = row_sum<G>(ss, red);
+  ss = row_sum<BLOCK>(ss, red);
   const float r = 1.f / sqrtf(ss / static_cast<float>(cols) + eps);
   if (rstd && t == 0) rstd[row] = r;
   const int col_tiles = (cols + F8_TILE_COLS - 1) / F8_TILE_COLS;
@@ -145,69 +148,49 @@ __global__ void __launch_bounds__(G > 32 ? G : 256)
   }
 }
 
-// dx = rstd (t - s rstd^2 mean(t s)) + dsum, t = dy gamma.  A row is held in
-// registers by G threads as above; a block (or warp) walks rows blockIdx.x,
-// blockIdx.x + gridDim.x, ..., and a thread's columns are the same in all of
-// them, so the sums of dy s rstd stay in registers and are written once per
-// block, as one row of `parts`.
-template <int G, int NV>
-__global__ void __launch_bounds__(G > 32 ? G : 256)
-    k_rmsnorm_bwd(const bf16* dy, const bf16* dsum, const bf16* __restrict__ sum,
-                  const float* __restrict__ gamma, const float* __restrict__ rstd, int64_t rows,
-                  int cols, bf16* dx, float* __restrict__ parts) {
-  __shared__ float red[2][32];
-  grid_dep_launch();
-  grid_dep_wait();
-  const int t = G > 32 ? threadIdx.x : (threadIdx.x & 31);
-  const int64_t first =
-      G > 32 ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  const int64_t step = G > 32 ? gridDim.x : static_cast<int64_t>(gridDim.x) * 8;
-  const int nvec = cols >> 3;
-  float acc[NV][8] = {};
-  int flip = 0;
-  for (int64_t row = first; row < rows; row += step, flip ^= 1) {
-    uint4 vd[NV], vs[NV];
-    const uint4 zero = make_uint4(0, 0, 0, 0);
+// dx = rstd (t - s rstd^2 mean(t s)) + dsum, t = dy gamma.
+//
+// One row's part of it, for the threads that hold the row in registers (NV
+// vectors of dy, s and dsum each): adds dy s rstd to acc and stores dx.
+template <int NV, bool BLOCK>
+__device__ __forceinline__ void bwd_row(const uint4 (&vd)[NV], const uint4 (&vs)[NV],
+                                        const uint4 (&ve)[NV], float r,
+                                        const float* __restrict__ gamma, int t, int G, int nvec,
+                                        int cols, float* red, float (&acc)[NV][8], bf16* out) {
+  float dot = 0.f;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int u = t + j * G;
-      vd[j] = u < nvec ? *reinterpret_cast<const uint4*>(dy + row * cols + 8 * u) : zero;
-      vs[j] = u < nvec ? *reinterpret_cast<const uint4*>(sum + row * cols + 8 * u) : zero;
-    }
-    const float r = rstd[row];
-    float dot = 0.f;
+  for (int j = 0; j < NV; ++j) {
+    const int u = t + j * G;
+    float d[8], s[8], g[8] = {};
+    unpack8_bits(vd[j], d);
+    unpack8_bits(vs[j], s);
+    if (u < nvec) load8(gamma + 8 * u, g);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int u = t + j * G;
-      float d[8], s[8], g[8] = {};
-      unpack8_bits(vd[j], d);
-      unpack8_bits(vs[j], s);
-      if (u < nvec) load8(gamma + 8 * u, g);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        dot += d[i] * g[i] * s[i];
-        acc[j][i] += d[i] * (s[i] * r);
-      }
-    }
-    dot = row_sum<G>(dot, red[flip]);
-    const float c = r * r * (dot / static_cast<float>(cols));
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int u = t + j * G;
-      if (u < nvec) {
-        float d[8], s[8], g[8], e[8] = {};
-        unpack8_bits(vd[j], d);
-        unpack8_bits(vs[j], s);
-        load8(gamma + 8 * u, g);
-        if (dsum) unpack8_bits(*reinterpret_cast<const uint4*>(dsum + row * cols + 8 * u), e);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) d[i] = r * (d[i] * g[i] - s[i] * c) + e[i];
-        *reinterpret_cast<uint4*>(dx + row * cols + 8 * u) = pack8(d);
-      }
+    for (int i = 0; i < 8; ++i) {
+      dot += d[i] * g[i] * s[i];
+      acc[j][i] += d[i] * (s[i] * r);
     }
   }
-  if (!parts) return;
-  float* p = parts + (G > 32 ? static_cast<size_t>(blockIdx.x) : static_cast<size_t>(first)) * cols;
+  dot = row_sum<BLOCK>(dot, red);
+  const float c = r * r * (dot / static_cast<float>(cols));
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int u = t + j * G;
+    if (u < nvec) {
+      float d[8], s[8], g[8], e[8];
+      unpack8_bits(vd[j], d);
+      unpack8_bits(vs[j], s);
+      unpack8_bits(ve[j], e);
+      load8(gamma + 8 * u, g);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) d[i] = r * (d[i] * g[i] - s[i] * c) + e[i];
+      *reinterpret_cast<uint4*>(out + 8 * u) = pack8(d);
+    }
+  }
+}
+template <int NV>
+__device__ __forceinline__ void put_acc(const float (&acc)[NV][8], int t, int G, int nvec,
+                                        float* p) {
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int u = t + j * G;
@@ -220,92 +203,267 @@ __global__ void __launch_bounds__(G > 32 ? G : 256)
   }
 }
 
-// out[c] = sum over n rows of parts[.][c], in a fixed order: 32 columns per
-// block, 16 groups of rows, then the groups.
-__global__ void __launch_bounds__(512)
-    k_sum_parts(const float* __restrict__ parts, int n, int cols, float* __restrict__ out) {
-  __shared__ float red[16][33];
+// The gradient with rows brought to shared memory by bulk copies, `stages` rows
+// of this block ahead.  A block walks rows blockIdx.x, blockIdx.x + gridDim.x,
+// ...; a thread's columns are the same in all of them, so the sums of dy s rstd
+// stay in registers and each block writes one row of `parts` at its end.
+// Bound by its bytes (dy, s, dsum, dx: 8 per column).  Loads into registers one
+// row ahead instead took 107 registers, which leaves one block of nine warps
+// per SM (33 us at 4001 x 4112); at 96 the compiler gave up the look-ahead.
+template <int NV>
+__global__ void __launch_bounds__(NV == 1 ? 1024 : 512)
+    k_rmsnorm_bwd_staged(const bf16* dy, const bf16* dsum, const bf16* sum,
+                         const float* __restrict__ gamma, const float* __restrict__ rstd,
+                         int64_t rows, int cols, bf16* dx, float* __restrict__ parts, int stages,
+                         int* status) {
+  __shared__ float red[2][32];
+  __shared__ alignas(8) uint64_t bars[8];
+  __shared__ int abort_word;
+  extern __shared__ __align__(16) uint8_t ring[];
+  volatile int* abort_flag = &abort_word;
+  const int t = threadIdx.x, G = blockDim.x;
+  const int nvec = cols >> 3;
+  const uint32_t row_bytes = 2 * cols;
+  const int arrays = dsum ? 3 : 2;
+  const uint32_t stage_bytes = arrays * row_bytes;
+  if (t == 0) {
+    for (int i = 0; i < stages; ++i) mbar_init(smem_u32(bars + i), 1);
+    abort_word = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+  }
+  __syncthreads();
   grid_dep_launch();
   grid_dep_wait();
-  const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
-  float a = 0.f;
-  if (c < cols)
-    for (int i = grp; i < n; i += 16) a += parts[static_cast<size_t>(i) * cols + c];
-  red[grp][lane] = a;
-  __syncthreads();
-  if (grp == 0 && c < cols) {
+  if (t == 0 && blockIdx.x == 0) *status = 0;
+  auto fetch = [&](int64_t row, uint32_t slot) {  // thread 0
+    const uint32_t bar = smem_u32(bars + slot), dst = smem_u32(ring) + slot * stage_bytes;
+    mbar_arrive_expect_tx(bar, stage_bytes);
+    bulk_load(dst, dy + row * cols, row_bytes, bar);
+    bulk_load(dst + row_bytes, sum + row * cols, row_bytes, bar);
+    if (dsum) bulk_load(dst + 2 * row_bytes, dsum + row * cols, row_bytes, bar);
+  };
+  if (t == 0) {
+    int64_t row = blockIdx.x;
+    for (int i = 0; i < stages && row < rows; ++i, row += gridDim.x) fetch(row, i);
+  }
+  float acc[NV][8] = {};
+  RingPos r;
+  int flip = 0;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, r.next(stages), flip ^= 1) {
+    const float rs = rstd[row];
+    // a wait that runs out leaves the rest of the call meaningless, not stuck
+    mbar_wait(smem_u32(bars + r.slot), r.phase, status, abort_flag);
+    const uint8_t* at = ring + r.slot * stage_bytes;
+    uint4 vd[NV], vs[NV], ve[NV];
 #pragma unroll
-    for (int i = 1; i < 16; ++i) a += red[i][lane];
+    for (int j = 0; j < NV; ++j) {
+      const int u = t + j * G;
+      const bool live = u < nvec;
+      vd[j] = live ? *reinterpret_cast<const uint4*>(at + 16 * u) : zero;
+      vs[j] = live ? *reinterpret_cast<const uint4*>(at + row_bytes + 16 * u) : zero;
+      ve[j] = live && dsum ? *reinterpret_cast<const uint4*>(at + 2 * row_bytes + 16 * u) : zero;
+    }
+    // every thread has its part of the row before row_sum's barrier, so the
+    // slot is free after it
+    bwd_row<NV, true>(vd, vs, ve, rs, gamma, t, G, nvec, cols, red[flip], acc, dx + row * cols);
+    const int64_t next = row + static_cast<int64_t>(stages) * gridDim.x;
+    if (t == 0 && next < rows && !*abort_flag) fetch(next, r.slot);
+  }
+  if (parts) put_acc<NV>(acc, t, G, nvec, parts + static_cast<size_t>(blockIdx.x) * cols);
+  __syncthreads();
+  if (*abort_flag)  // copies already in flight land before the block ends
+    for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+}
+
+// The same with the rows loaded as they come: by a warp per row (up to 512
+// columns, eight rows per block, whose sums are joined at the end), or by a
+// block for rows of which shared memory does not hold two.
+template <int NV, bool BLOCK>
+__global__ void __launch_bounds__(BLOCK ? 1024 : 256)
+    k_rmsnorm_bwd(const bf16* dy, const bf16* dsum, const bf16* sum,
+                  const float* __restrict__ gamma, const float* __restrict__ rstd, int64_t rows,
+                  int cols, bf16* dx, float* __restrict__ parts, int* status) {
+  __shared__ float red[2][32];
+  extern __shared__ float joined[];  // warps' rows: [8][cols] of their sums
+  grid_dep_launch();
+  grid_dep_wait();
+  if (threadIdx.x == 0 && blockIdx.x == 0) *status = 0;
+  const int G = BLOCK ? blockDim.x : 32;
+  const int t = BLOCK ? threadIdx.x : (threadIdx.x & 31);
+  const int64_t first =
+      BLOCK ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int64_t step = BLOCK ? gridDim.x : static_cast<int64_t>(gridDim.x) * 8;
+  const int nvec = cols >> 3;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  float acc[NV][8] = {};
+  int flip = 0;
+  for (int64_t row = first; row < rows; row += step, flip ^= 1) {
+    uint4 vd[NV], vs[NV], ve[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int u = t + j * G;
+      const int64_t at = row * cols + 8 * u;
+      vd[j] = u < nvec ? *reinterpret_cast<const uint4*>(dy + at) : zero;
+      vs[j] = u < nvec ? *reinterpret_cast<const uint4*>(sum + at) : zero;
+      ve[j] = u < nvec && dsum ? *reinterpret_cast<const uint4*>(dsum + at) : zero;
+    }
+    bwd_row<NV, BLOCK>(vd, vs, ve, rstd[row], gamma, t, G, nvec, cols, red[flip], acc,
+                       dx + row * cols);
+  }
+  if (!parts) return;
+  if (BLOCK) {
+    put_acc<NV>(acc, t, G, nvec, parts + static_cast<size_t>(blockIdx.x) * cols);
+  } else {
+    put_acc<NV>(acc, t, G, nvec, joined + (threadIdx.x >> 5) * cols);
+    __syncthreads();
+    for (int c = threadIdx.x; c < cols; c += 256) {
+      float a = 0.f;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) a += joined[w * cols + c];
+      parts[static_cast<size_t>(blockIdx.x) * cols + c] = a;
+    }
+  }
+}
+
+// out[c] = sum over n rows of parts[.][c], in a fixed order: 8 columns (one
+// sector) per block, 64 groups of rows.
+__global__ void __launch_bounds__(512)
+    k_sum_parts(const float* __restrict__ parts, int n, int cols, float* __restrict__ out) {
+  __shared__ float red[16][8];
+  grid_dep_launch();
+  grid_dep_wait();
+  const int c = blockIdx.x * 8 + (threadIdx.x & 7), grp = threadIdx.x >> 3;
+  float a = 0.f;
+#pragma unroll 8
+  for (int i = grp; i < n; i += 64) a += parts[static_cast<size_t>(i) * cols + c];
+  a += __shfl_xor_sync(0xFFFFFFFFu, a, 8);
+  a += __shfl_xor_sync(0xFFFFFFFFu, a, 16);
+  if ((threadIdx.x & 31) < 8) red[threadIdx.x >> 5][threadIdx.x & 7] = a;
+  __syncthreads();
+  if (threadIdx.x < 8) {
+    a = 0.f;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) a += red[w][threadIdx.x];
     out[c] = a;
   }
 }
 
-// 16 lanes per 128-column block, 8 values each.
+// 16 lanes per 128-column block, 8 values each, QUANT_U blocks of a lane in
+// flight.  The largest magnitude is found on the bf16 bits, two values at a
+// time (without their signs they order like integers); only a block that holds
+// a NaN or an infinity, whose bits are the largest of all, looks again.
+// DIV: a type that can count all blocks.
+constexpr int QUANT_U = 4;
+template <typename DIV>
 __global__ void __launch_bounds__(256)
-    k_f8_quant(const bf16* __restrict__ x, int64_t rows, int cols, int e5m2,
+    k_f8_quant(const bf16* __restrict__ x, DIV total, uint32_t blocks, int cols, int e5m2,
                uint8_t* __restrict__ q, uint8_t* __restrict__ scales) {
   grid_dep_launch();
   grid_dep_wait();
-  const int blocks = (cols + F8_BLOCK - 1) / F8_BLOCK;
   const int col_tiles = (cols + F8_TILE_COLS - 1) / F8_TILE_COLS;
-  const int64_t total = rows * blocks;
   const int sub = threadIdx.x & 15;
   const uint32_t mask = 0xFFFFu << (threadIdx.x & 16);
-  for (int64_t b = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 4); b < total;
-       b += static_cast<int64_t>(gridDim.x) * 16) {
-    const int64_t row = b / blocks;
-    const int blk = static_cast<int>(b - row * blocks);
-    const int col = blk * F8_BLOCK + sub * 8;
-    float f[8] = {};
-    if (col < cols) unpack8_bits(*reinterpret_cast<const uint4*>(x + row * cols + col), f);
-    const uint32_t s = f8_scale_byte(block_amax(f, mask), e5m2);
+  const DIV first = static_cast<DIV>(blockIdx.x) * (16 * QUANT_U) + (threadIdx.x >> 4);
+  uint4 v[QUANT_U];
+  int64_t row[QUANT_U];
+  int blk[QUANT_U];
+#pragma unroll
+  for (int k = 0; k < QUANT_U; ++k) {
+    const DIV b = first + 16 * k;
+    const DIV r = b / blocks;
+    row[k] = static_cast<int64_t>(r);
+    blk[k] = static_cast<int>(b - r * blocks);
+    const int col = blk[k] * F8_BLOCK + sub * 8;
+    v[k] = b < total && col < cols ? *reinterpret_cast<const uint4*>(x + row[k] * cols + col)
+                                   : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int k = 0; k < QUANT_U; ++k) {
+    if (first + 16 * k >= total) break;  // the same for all 16 lanes
+    const int col = blk[k] * F8_BLOCK + sub * 8;
+    constexpr uint32_t MAG = 0x7FFF7FFFu;
+    uint32_t m = __vmaxu2(__vmaxu2(v[k].x & MAG, v[k].y & MAG), __vmaxu2(v[k].z & MAG, v[k].w & MAG));
+    m = max(m & 0xFFFFu, m >> 16);
+#pragma unroll
+    for (int o = 8; o; o >>= 1) m = max(m, __shfl_xor_sync(mask, m, o));
+    float f[8];
+    unpack8_bits(v[k], f);
+    const float a = m < 0x7F80u ? __uint_as_float(m << 16) : block_amax(f, mask);
+    const uint32_t s = f8_scale_byte(a, e5m2);
     if (col < cols)
-      *reinterpret_cast<uint2*>(q + row * cols + col) = codes8(f, f8_scale_inv(s), e5m2);
-    if (sub == 0) scales[f8_scale_at(row, blk, col_tiles)] = static_cast<uint8_t>(s);
+      *reinterpret_cast<uint2*>(q + row[k] * cols + col) = codes8(f, f8_scale_inv(s), e5m2);
+    if (sub == 0) scales[f8_scale_at(row[k], blk[k], col_tiles)] = static_cast<uint8_t>(s);
   }
 }
 
 // 16 codes per thread.
 __global__ void __launch_bounds__(256)
-    k_f8_dequant(const uint8_t* __restrict__ q, const uint8_t* __restrict__ scales, int64_t rows,
-                 int cols, int e5m2, bf16* __restrict__ x) {
+    k_f8_dequant(const uint8_t* __restrict__ q, const uint8_t* __restrict__ scales, int64_t total,
+                 uint32_t vecs, int cols, int e5m2, bf16* __restrict__ x) {
   grid_dep_launch();
   grid_dep_wait();
-  const int vecs = cols >> 4;
   const int col_tiles = (cols + F8_TILE_COLS - 1) / F8_TILE_COLS;
-  const int64_t total = rows * vecs;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total;
-       i += static_cast<int64_t>(gridDim.x) * 256) {
-    const int64_t row = i / vecs;
-    const int c = static_cast<int>(i - row * vecs);
-    const uint4 w = *reinterpret_cast<const uint4*>(q + i * 16);
-    const float sc = f8_scale_val(scales[f8_scale_at(row, c >> 3, col_tiles)]);
-    uint32_t o[8];
-    const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * 256;
+  const int64_t i = first + threadIdx.x;
+  if (i >= total) return;
+  const uint4 w = *reinterpret_cast<const uint4*>(q + i * 16);
+  const int64_t row0 = first / vecs;
+  const uint32_t c0 = static_cast<uint32_t>(first - row0 * vecs) + threadIdx.x;
+  const uint32_t down = c0 / vecs;
+  const float sc =
+      f8_scale_val(scales[f8_scale_at(row0 + down, (c0 - down * vecs) >> 3, col_tiles)]);
+  uint32_t o[8];
+  const uint32_t in[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      float v[4];
-      f8_unpack4(in[k], e5m2, v);
-      o[2 * k] = pack_bf16(v[0] * sc, v[1] * sc);
-      o[2 * k + 1] = pack_bf16(v[2] * sc, v[3] * sc);
-    }
-    uint4* out = reinterpret_cast<uint4*>(x + i * 16);
-    out[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    out[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  for (int n = 0; n < 4; ++n) {
+    float v[4];
+    f8_unpack4(in[n], e5m2, v);
+    o[2 * n] = pack_bf16(v[0] * sc, v[1] * sc);
+    o[2 * n + 1] = pack_bf16(v[2] * sc, v[3] * sc);
   }
+  uint4* out = reinterpret_cast<uint4*>(x + i * 16);
+  out[0] = make_uint4(o[0], o[1], o[2], o[3]);
+  out[1] = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
-int grid_for(int64_t blocks) {
-  const int64_t most = static_cast<int64_t>(ff_num_sms()) * 16;
-  return static_cast<int>(blocks < most ? blocks : most);
+// How a row is held: up to 512 columns by a warp (no block barrier), beyond by
+// a block of as many warps as NV vectors per thread need.
+struct RowShape {
+  int nv, threads;
+  bool block;
+};
+RowShape row_shape(int cols) {
+  const int nvec = cols >> 3;
+  if (nvec <= 64) return {nvec <= 32 ? 1 : 2, 256, false};
+  const int nv = nvec <= 1024 ? 2 : (nvec <= 2048 ? 4 : 8);
+  return {nv, ((nvec + nv - 1) / nv + 31) / 32 * 32, true};
 }
 
-// Blocks of the backward: as many rows in flight as the SMs hold.
-int bwd_grid(int64_t rows, int cols) {
-  const int64_t want = cols <= 1024 ? (rows + 7) / 8 : rows;
-  const int64_t most = static_cast<int64_t>(ff_num_sms()) * (cols <= 8192 ? 2 : 1);
-  return static_cast<int>(want < most ? want : most);
+// How the backward runs: blocks, and how many rows a block keeps in shared
+// memory (0: none).  About 640 threads per SM share 220 KB.
+struct BwdShape {
+  int grid, stages;
+};
+RowShape bwd_row_shape(int cols) {
+  const int nvec = cols >> 3;
+  RowShape r = row_shape(cols);
+  if (r.block && nvec <= 1024) r = {1, (nvec + 31) / 32 * 32, true};
+  return r;
+}
+BwdShape bwd_shape(int64_t rows, int cols) {
+  const RowShape r = bwd_row_shape(cols);
+  const int64_t want = r.block ? rows : (rows + 7) / 8;
+  const int room = r.nv == 1 ? 1152 : 640;
+  const int per_sm = r.threads > room ? 1 : room / r.threads;
+  const int64_t most = static_cast<int64_t>(ff_num_sms()) * per_sm;
+  BwdShape b;
+  b.grid = static_cast<int>(want < most ? want : most);
+  b.stages = r.block && r.nv <= 4 ? 220 * 1024 / per_sm / (6 * cols) : 0;
+  if (b.stages > 6) b.stages = 6;
+  if (b.stages < 2) b.stages = 0;
+  return b;
 }
 
 }  // namespace
@@ -323,47 +481,51 @@ int ff_num_sms() {
   return cached[dev];
 }
 
-// Threads per row by its width: a warp up to 1024 columns (no block
-// barrier, eight rows per block), 256 threads up to 16384, 1024 beyond.
-#define ALX_ROWS(G_, NV_, KERNEL, GRID, ...) \
-  e = ff_launch(KERNEL<G_, NV_>, GRID, G_ > 32 ? G_ : 256, 0, 0, s, __VA_ARGS__)
-#define ALX_ROWS_BY_WIDTH(KERNEL, WARP_GRID, ROW_GRID, ...)                       \
-  if (cols <= 256) ALX_ROWS(32, 1, KERNEL, WARP_GRID, __VA_ARGS__);               \
-  else if (cols <= 512) ALX_ROWS(32, 2, KERNEL, WARP_GRID, __VA_ARGS__);          \
-  else if (cols <= 1024) ALX_ROWS(32, 4, KERNEL, WARP_GRID, __VA_ARGS__);         \
-  else if (cols <= 2048) ALX_ROWS(256, 1, KERNEL, ROW_GRID, __VA_ARGS__);         \
-  else if (cols <= 4096) ALX_ROWS(256, 2, KERNEL, ROW_GRID, __VA_ARGS__);         \
-  else if (cols <= 8192) ALX_ROWS(256, 4, KERNEL, ROW_GRID, __VA_ARGS__);         \
-  else if (cols <= 16384) ALX_ROWS(256, 8, KERNEL, ROW_GRID, __VA_ARGS__);        \
-  else if (cols <= 32768) ALX_ROWS(1024, 4, KERNEL, ROW_GRID, __VA_ARGS__);       \
-  else ALX_ROWS(1024, 8, KERNEL, ROW_GRID, __VA_ARGS__)
-
 cudaError_t launch_rmsnorm_fwd(const bf16* x, const bf16* res, const float* gamma, int64_t rows,
                                int cols, float eps, bf16* sum, bf16* y, float* rstd, uint8_t* q,
                                uint8_t* scales, cudaStream_t s) {
-  const int64_t wg = (rows + 7) / 8, rg = rows;
-  cudaError_t e = cudaSuccess;
-  ALX_ROWS_BY_WIDTH(k_rmsnorm_fwd, wg, rg, x, res, gamma, rows, cols, eps, sum, y, rstd, q,
-                    scales);
+  const RowShape rs = row_shape(cols);
+  const int64_t grid = rs.block ? rows : (rows + 7) / 8;
+  auto* kernel = !rs.block ? (rs.nv == 1 ? k_rmsnorm_fwd<1, false> : k_rmsnorm_fwd<2, false>)
+                           : (rs.nv == 2   ? k_rmsnorm_fwd<2, true>
+                              : rs.nv == 4 ? k_rmsnorm_fwd<4, true>
+                                           : k_rmsnorm_fwd<8, true>);
   count_launch();
-  return e;
+  return ff_launch(kernel, grid, rs.threads, 0, 0, s, x, res, gamma, rows, cols, eps, sum, y, rstd,
+                   q, scales);
 }
 
 int rmsnorm_bwd_parts(int64_t rows, int cols) {
-  return bwd_grid(rows, cols) * (cols <= 1024 ? 8 : 1);
+  return bwd_shape(rows, cols).grid;
 }
 
 cudaError_t launch_rmsnorm_bwd(const bf16* dy, const bf16* dsum, const bf16* sum,
                                const float* gamma, const float* rstd, int64_t rows, int cols,
-                               bf16* dx, float* dgamma, float* parts, cudaStream_t s) {
-  const int grid = bwd_grid(rows, cols);
+                               bf16* dx, float* dgamma, float* parts, int* status,
+                               cudaStream_t s) {
+  const RowShape rs = bwd_row_shape(cols);
+  const BwdShape bs = bwd_shape(rows, cols);
+  float* into = dgamma ? parts : nullptr;
   cudaError_t e = cudaSuccess;
-  ALX_ROWS_BY_WIDTH(k_rmsnorm_bwd, grid, grid, dy, dsum, sum, gamma, rstd, rows, cols, dx,
-                    dgamma ? parts : static_cast<float*>(nullptr));
   count_launch();
+  if (bs.stages) {
+    const int smem = bs.stages * (dsum ? 6 : 4) * cols;
+    static bool ready1[64] = {}, ready4[64] = {};
+    e = rs.nv == 1 ? ff_all_smem(k_rmsnorm_bwd_staged<1>, ready1, 1024)
+                   : ff_all_smem(k_rmsnorm_bwd_staged<4>, ready4, 1024);
+    if (e == cudaSuccess)
+      e = ff_launch(rs.nv == 1 ? k_rmsnorm_bwd_staged<1> : k_rmsnorm_bwd_staged<4>, bs.grid,
+                    rs.threads, smem, 0, s, dy, dsum, sum, gamma, rstd, rows, cols, dx, into,
+                    bs.stages, status);
+  } else if (rs.block) {
+    e = ff_launch(k_rmsnorm_bwd<8, true>, bs.grid, rs.threads, 0, 0, s, dy, dsum, sum, gamma, rstd,
+                  rows, cols, dx, into, status);
+  } else {
+    e = ff_launch(rs.nv == 1 ? k_rmsnorm_bwd<1, false> : k_rmsnorm_bwd<2, false>, bs.grid, 256,
+                  8 * cols * 4, 0, s, dy, dsum, sum, gamma, rstd, rows, cols, dx, into, status);
+  }
   if (dgamma && e == cudaSuccess) {
-    e = ff_launch(k_sum_parts, (cols + 31) / 32, 512, 0, 0, s, parts,
-                  rmsnorm_bwd_parts(rows, cols), cols, dgamma);
+    e = ff_launch(k_sum_parts, cols / 8, 512, 0, 0, s, parts, bs.grid, cols, dgamma);
     count_launch();
   }
   return e;
@@ -371,17 +533,23 @@ cudaError_t launch_rmsnorm_bwd(const bf16* dy, const bf16* dsum, const bf16* sum
 
 cudaError_t launch_f8_quant(const bf16* x, int64_t rows, int cols, int e5m2, uint8_t* q,
                             uint8_t* scales, cudaStream_t s) {
-  const int64_t blocks = rows * ((cols + F8_BLOCK - 1) / F8_BLOCK);
+  const int blocks = (cols + F8_BLOCK - 1) / F8_BLOCK;
+  const int64_t total = rows * blocks;
+  const int64_t grid = (total + 16 * QUANT_U - 1) / (16 * QUANT_U);
   count_launch();
-  return ff_launch(k_f8_quant, grid_for((blocks + 15) / 16), 256, 0, 0, s, x, rows, cols, e5m2, q,
+  if (total < (1ll << 31))
+    return ff_launch(k_f8_quant<uint32_t>, grid, 256, 0, 0, s, x, total, blocks, cols, e5m2, q,
+                     scales);
+  return ff_launch(k_f8_quant<uint64_t>, grid, 256, 0, 0, s, x, total, blocks, cols, e5m2, q,
                    scales);
 }
 
 cudaError_t launch_f8_dequant(const uint8_t* q, const uint8_t* scales, int64_t rows, int cols,
                               int e5m2, bf16* x, cudaStream_t s) {
-  const int64_t vecs = rows * (cols >> 4);
+  const int vecs = cols >> 4;
+  const int64_t total = rows * vecs;
   count_launch();
-  return ff_launch(k_f8_dequant, grid_for((vecs + 255) / 256), 256, 0, 0, s, q, scales, rows, cols,
+  return ff_launch(k_f8_dequant, (total + 255) / 256, 256, 0, 0, s, q, scales, total, vecs, cols,
                    e5m2, x);
 }
 
