@@ -29,6 +29,10 @@ struct FfProduct {
   GateSave save;
   int* status;   // bit 0: a bounded wait ran out;
   int fresh;     // set it to 0 first
+  // > 0: independent of the pair launch just before it in the stream, which has
+  // so many tiles of so many steps of K; what that launch waited for is all
+  // that this one depends on
+  int beside_tiles, beside_steps;
 };
 
 // Both run the product and set *err to the launch's error; false where the

@@ -203,10 +203,16 @@ alexnet_status gated_bwd(const void* dh, const void* x, const GateSave& save, in
   bf16* dz = reinterpret_cast<bf16*>(U8(ws) + 256);
   int* status = static_cast<int*>(ws);
   if (cudaError_t e = launch_gate_bwd(B16(dh), save, B, F, act, dz, status, s)) return done(e);
-  if (dx)
-    if (alexnet_status e = product(bf16_product(dz, 0, w, 1, B, In, 2 * F, dx, status), s))
-      return e;
-  return dw ? product(bf16_product(dz, 1, x, 1, 2 * F, In, B, dw, status), s) : ALEXNET_OK;
+  FfProduct d = bf16_product(dz, 1, x, 1, 2 * F, In, B, dw, status);
+  if (dx) {
+    const FfProduct q = bf16_product(dz, 0, w, 1, B, In, 2 * F, dx, status);
+    if (alexnet_status e = product(q, s)) return e;
+    if (!runs_narrow(q)) {
+      d.beside_tiles = ((B + 255) / 256) * ((In + 255) / 256);
+      d.beside_steps = (2 * F + 63) / 64;
+    }
+  }
+  return dw ? product(d, s) : ALEXNET_OK;
 }
 
 }  // namespace

@@ -48,11 +48,24 @@ struct PairArgs {
   int k_tiles;           // scale tiles per 128 rows
   int act, wide;         // wide: 32-byte stores are aligned
   int fresh;             // clear the status word first
+  int beside;            // independent of the launch before it: wait for that at the end
+  int rounds, early;     // tile_of
   uint32_t idesc;
   void* out;
   GateSave save;
   int* status;
 };
+
+// The i-th tile of pair c of `pairs`: one per pair and round, then the rest
+// among the first `early` pairs (usually all).  -1: none.
+__device__ __forceinline__ int tile_of(const PairArgs& a, int total, int i, int c, int pairs) {
+  int t = c + i * pairs;
+  if (i >= a.rounds) {
+    if (c >= a.early) return -1;
+    t = a.rounds * pairs + c + (i - a.rounds) * a.early;
+  }
+  return t < total ? t : -1;
+}
 
 // Tiles in bands of 8 rows of tiles, column by column inside a band: the
 // tiles that run at one time then share few rows of A and B, which stay in L2.
@@ -212,12 +225,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  // The next launch may start once every pair is past its wait, that is, once
+  // all that this launch depends on is done: a launch with `beside` that
+  // follows has no need to wait for more until its end.
+  if (!args.beside) grid_dep_wait();
   grid_dep_launch();
-  grid_dep_wait();
   if (args.fresh && blockIdx.x == 0 && threadIdx.x == 0) *args.status = 0;
 
   const int total = args.m_tiles * args.n_tiles;
-  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
   if (warp == 8) {
     // ------------------------------------------------------------ producer
@@ -228,7 +244,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       RingPos r;
       int loaded = 0;
       bool ok = true;
-      for (int t = first; t < total && ok; t += step) {
+      for (int i = 0, t; ok && (t = tile_of(args, total, i, pair, pairs)) >= 0; ++i) {
         int m, n;
         tile_at(args, t, m, n);
         const int m0 = m * 256 + rank * 128;
@@ -286,7 +302,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       RingPos r;
       uint32_t count = 0, scale_buf = 0;
       bool ok = true;
-      for (int t = first; t < total && ok; t += step, ++count) {
+      for (; ok && tile_of(args, total, count, pair, pairs) >= 0; ++count) {
         const uint32_t acc = count & 1;
         if (F8) {
           // the tile before this one has left the columns the two share
@@ -338,7 +354,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const int quarter = warp & 3, half = warp >> 2;
     const uint32_t empty0 = map_rank(bar_acc_empty, 0);
     uint32_t count = 0;
-    for (int t = first; t < total; t += step, ++count) {
+    for (int t; (t = tile_of(args, total, count, pair, pairs)) >= 0; ++count) {
       int m, n;
       tile_at(args, t, m, n);
       const uint32_t acc = count & 1;
@@ -435,6 +451,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     // give bulk copies already in flight time to land before the CTA ends
     for (int i = 0; i < 1000; ++i) __nanosleep(1000);
   }
+  if (args.beside) grid_dep_wait();
   cluster_sync();
   if (warp == 9) {
     tc_fence_after();
@@ -510,6 +527,21 @@ bool ff_pair_product(const FfProduct& p, cudaStream_t s, cudaError_t* err) {
   const int pairs = ff_num_sms() / 2;
   const int tiles = a.m_tiles * a.n_tiles;
   const int grid = 2 * (tiles < pairs ? tiles : pairs);
+  a.rounds = 0x7FFFFFFF;
+  a.early = pairs;
+  a.beside = p.beside_tiles > 0;
+  if (a.beside && tiles > pairs && p.beside_tiles % pairs) {
+    // The launch before this one has `beside_tiles` tiles of beside_steps steps:
+    // in its last round only some pairs are busy, and the others start here
+    // that much earlier.  They are the first to be launched, so the first pairs
+    // get that many tiles more.
+    const int idle = pairs - p.beside_tiles % pairs;
+    const int64_t more = static_cast<int64_t>(p.beside_steps) * idle / a.kblocks;
+    if (more < tiles) {
+      a.rounds = static_cast<int>((tiles - more) / pairs);
+      a.early = idle;
+    }
+  }
 #define ALX_PAIR(F8_, AM_, BM_, OUT_)                                              \
   if (p.f8 == F8_ && p.a_mn == AM_ && p.b_mn == BM_ && p.out_kind == OUT_) {       \
     *err = launch<F8_, AM_, BM_, OUT_>(tm, a, stages, smem, grid, s);              \
