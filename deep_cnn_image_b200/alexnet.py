@@ -135,11 +135,7 @@ lib, EXPORTED = _load()
 
 
 def _ptr(t):
-    if t is None:
-        return None
-    if isinstance(t, int):
-        return t
-    return t.data_ptr()
+    return t if t is None or t.__class__ is int else t.data_ptr()
 
 
 def _stream(stream):

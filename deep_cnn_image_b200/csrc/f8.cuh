@@ -72,4 +72,20 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&h);
 }
 
+// 16 codes times a scale as bf16, 32 bytes.
+__device__ __forceinline__ void f8_expand16(const uint4& w, float sc, int e5m2,
+                                            __nv_bfloat16* out) {
+  uint32_t o[8];
+  const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int n = 0; n < 4; ++n) {
+    float v[4];
+    f8_unpack4(in[n], e5m2, v);
+    o[2 * n] = pack_bf16(v[0] * sc, v[1] * sc);
+    o[2 * n + 1] = pack_bf16(v[2] * sc, v[3] * sc);
+  }
+  reinterpret_cast<uint4*>(out)[0] = make_uint4(o[0], o[1], o[2], o[3]);
+  reinterpret_cast<uint4*>(out)[1] = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
 }  // namespace alx

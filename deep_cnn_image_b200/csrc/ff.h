@@ -74,11 +74,17 @@ struct GateSave {
   bf16* b16;      // [B, 2F]
   uint8_t* q;     // two 8-bit matrices [B, F], one after the other,
   uint8_t* qs;    // and their scales
+  // with q, for the backward: the block's input as 8-bit rows [B, In] and where
+  // its values go (null: not wanted)
+  const uint8_t *xq, *xs;
+  bf16* xb;
+  int In;
 };
 // z fp32 [B, 2F] -> h, and z in what `save` holds
 cudaError_t launch_gate_fwd(const float* z, int B, int F, int act, bf16* h, const GateSave& save,
                             cudaStream_t s);
-// dz bf16 [B, 2F] from dh and the saved projections; *status = 0
+// dz bf16 [B, 2F] from dh and the saved projections, and the saved input's
+// values; *status = 0
 cudaError_t launch_gate_bwd(const bf16* dh, const GateSave& save, int B, int F, int act, bf16* dz,
                             int* status, cudaStream_t s);
 

@@ -42,7 +42,10 @@ bool runs_narrow(const FfProduct& p) {
   if (p.a_mn) return false;
   const int rows = p.out_kind == FF_GATED ? 2 * p.N : p.N;
   const int kblocks = ((p.f8 ? p.K : 2 * p.K) + 127) / 128;
-  return ff_narrow_plan(p.M, rows, kblocks).ns < ff_pair_ns(p.M, rows, kblocks);
+  // with 8-bit checkpoints the narrow kernel leaves gate and codes to a second
+  // one (5 us at 333 tokens); the block takes one way whatever it keeps
+  const double more = p.out_kind == FF_GATED && p.M > 128 ? 3000 : 0;
+  return ff_narrow_plan(p.M, rows, kblocks).ns + more < ff_pair_ns(p.M, rows, kblocks);
 }
 
 alexnet_status product(const FfProduct& p, cudaStream_t s) {
@@ -191,7 +194,9 @@ alexnet_status gated_fwd(const void* x, int B, int In, const void* w, int F, int
     FfProduct both = bf16_product(x, 0, w, 0, B, 2 * F, In, z, static_cast<int*>(ws));
     both.out_kind = FF_F32;
     both.fresh = 1;
-    if (alexnet_status e = product(both, s)) return e;
+    cudaError_t e = cudaSuccess;
+    if (!ff_narrow_product(both, s, &e)) return ALEXNET_ERR_UNSUPPORTED;
+    if (e) return done(e);
     return done(launch_gate_fwd(z, B, F, act, B16(h), save, s));
   }
   return product(p, s);
@@ -261,11 +266,10 @@ alexnet_status alexnet_op_gated_bwd_ckpt8(const void* dh, const void* xq, const 
     return ALEXNET_ERR_INVALID_ARG;
   if (In > MAX_DIM || F > MAX_DIM) return ALEXNET_ERR_UNSUPPORTED;
   if (!ws || ws_bytes < alexnet_gated_workspace_bytes(B, In, F)) return ALEXNET_ERR_INVALID_ARG;
+  GateSave save = save_of(guq, gus);
   bf16* xb = reinterpret_cast<bf16*>(U8(ws) + 256 + up256(8ull * B * F));
-  if (dw)
-    if (cudaError_t e = launch_f8_dequant(U8(xq), xs, B, In, ALEXNET_E4M3, xb, cu(stream)))
-      return done(e);
-  return gated_bwd(dh, xb, save_of(guq, gus), B, In, w, F, act, dx, dw, ws, cu(stream));
+  if (dw) save.xq = U8(xq), save.xs = xs, save.xb = xb, save.In = In;
+  return gated_bwd(dh, xb, save, B, In, w, F, act, dx, dw, ws, cu(stream));
 }
 
 }  // extern "C"

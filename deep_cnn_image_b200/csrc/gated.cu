@@ -82,7 +82,8 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// dg = dh u a'(g), du = dh a(g); 8 columns per thread, the projections from
+// dg = dh u a'(g), du = dh a(g) (and, with 8-bit checkpoints, the expansion of
+// the saved input); 8 columns per thread, the projections from
 // bf16 (KIND 0), 8-bit rows (1) or fp32 (2).  Bound by its bytes: 6, 4 or 10
 // read and 4 written per element of h.
 template <int KIND>
@@ -142,6 +143,20 @@ __global__ void __launch_bounds__(256)
     bf16* o = dz + row * 2 * F + col;
     *reinterpret_cast<uint4*>(o) = make_uint4(og[0], og[1], og[2], og[3]);
     *reinterpret_cast<uint4*>(o + F) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
+  }
+  if (KIND == 1 && save.xb) {
+    // the same launch expands the saved input for the weight gradient
+    const int In = save.In, xvecs = In >> 4;
+    const int x_tiles = (In + F8_TILE_COLS - 1) / F8_TILE_COLS;
+    const int64_t xtotal = static_cast<int64_t>(B) * xvecs;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < xtotal;
+         i += static_cast<int64_t>(gridDim.x) * 256) {
+      const int64_t row = i / xvecs;
+      const int c = static_cast<int>(i - row * xvecs);
+      const uint4 w = *reinterpret_cast<const uint4*>(save.xq + i * 16);
+      f8_expand16(w, f8_scale_val(save.xs[f8_scale_at(row, c >> 3, x_tiles)]), 0,
+                  save.xb + i * 16);
+    }
   }
 }
 

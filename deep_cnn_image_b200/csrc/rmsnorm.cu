@@ -414,18 +414,7 @@ __global__ void __launch_bounds__(256)
   const uint32_t down = c0 / vecs;
   const float sc =
       f8_scale_val(scales[f8_scale_at(row0 + down, (c0 - down * vecs) >> 3, col_tiles)]);
-  uint32_t o[8];
-  const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int n = 0; n < 4; ++n) {
-    float v[4];
-    f8_unpack4(in[n], e5m2, v);
-    o[2 * n] = pack_bf16(v[0] * sc, v[1] * sc);
-    o[2 * n + 1] = pack_bf16(v[2] * sc, v[3] * sc);
-  }
-  uint4* out = reinterpret_cast<uint4*>(x + i * 16);
-  out[0] = make_uint4(o[0], o[1], o[2], o[3]);
-  out[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  f8_expand16(w, sc, e5m2, x + i * 16);
 }
 
 // How a row is held: up to 512 columns by a warp (no block barrier), beyond by
