@@ -47,6 +47,7 @@ bool ff_narrow_product(const FfProduct& p, cudaStream_t s, cudaError_t* err);
 // time.
 struct FfNarrowPlan {
   int bn, tiles, split;
+  bool two;  // two CTAs per SM
   double ns;
 };
 FfNarrowPlan ff_narrow_plan(int tokens, int rows, int kblocks);

@@ -8,11 +8,15 @@
 // (token tiles) x S: a cluster of S <= 8 CTAs splits the reduction of one tile,
 // so that all SMs stream weights even where there are few tiles.  Each CTA
 // runs its slice of K through a ring of TMA stages into one accumulator in
-// tensor memory, puts it into its shared memory as [token][row], and the
-// cluster's CTAs add up the S copies through distributed shared memory, each
-// for its share of the tokens, in a fixed order; no partial sum reaches
-// memory and nothing depends on timing.  Rows of the weights are consecutive
-// columns of the result, so a token's 128 results leave as one run.
+// tensor memory.  The cluster's CTAs share the tokens out between them; each
+// writes its partial sums, as [token][row], into the shared memory of the CTA
+// that has the token, and after one cluster barrier every CTA adds up the S
+// copies that it holds, in a fixed order: no partial sum reaches memory and
+// nothing depends on timing.  (Reading the copies from the other CTAs instead
+// took 1 us more per call: a read waits about 500 clocks, a write for nothing,
+// and no second barrier has to keep the read memory alive.)  Rows of the
+// weights are consecutive columns of the result, so a token's 128 results leave
+// as one run.
 //
 // Roles (320 threads): warps 0-7 epilogue, warp 8 TMA producer, warp 9 MMA
 // issuer and TMEM owner.
@@ -123,6 +127,11 @@ __global__ void __launch_bounds__(THREADS)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  if (S > 1) cluster_arrive();  // this CTA runs: the others may write to it
+  const int tokens = min(BN, args.tokens - tt * BN);  // of this tile
+  const int share = (BN + S - 1) / S;                 // of them per CTA
+  // where the partial sums go: S copies of [share][128], behind the barriers
+  const uint32_t copies = S == 1 ? sW : bar_full + 256;
   grid_dep_launch();
   if (warp == 8 && lane == 0) {
     tma_prefetch_desc(&tmW);
@@ -211,69 +220,74 @@ __global__ void __launch_bounds__(THREADS)
       if (ok) tc_commit(bar_acc);
     }
   } else {
-    // accumulator -> shared memory as [token][row] (the stages are free: all
-    // products that read them are done)
-    float* acc = reinterpret_cast<float*>(smem);
+    // accumulator -> shared memory as [token][row]: with S = 1 in place of the
+    // stages (all products that read them are done), else in the copy number
+    // `rank` of the CTA that has the token
     if (__all_sync(0xFFFFFFFFu, mbar_wait(bar_acc, 0, args.status, abort_flag))) {
       tc_fence_after();
       const int row = (warp & 3) * 32 + lane;
       const uint32_t tb = tmem_base + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+      if (S > 1) cluster_wait();
 #pragma unroll
       for (int c = (warp >> 2) * 16; c < BN; c += 32) {
+        if (c >= tokens) break;
         float v[16];
         tmem_ld16(tb + c, v);
+        if (S == 1) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) acc[(c + i) * 128 + row] = v[i];
+          for (int i = 0; i < 16; ++i)
+            if (c + i < tokens) st_shared_f(copies + ((c + i) * 128 + row) * 4, v[i]);
+        } else {
+          int owner = c / share, at = c - owner * share;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            if (c + i < tokens)
+              st_cluster_f(map_rank(copies + ((rank * share + at) * 128 + row) * 4, owner), v[i]);
+            if (++at == share) at = 0, ++owner;
+          }
+        }
       }
       tc_fence_before();
+    } else if (S > 1) {
+      cluster_wait();
     }
   }
-  if (S > 1)
+  if (S > 1) {
+    if (warp >= 8) cluster_wait();
     cluster_sync();
-  else
+  } else {
     __syncthreads();
+  }
 
   // A thread adds up four rows (gated: four gate rows and the four up rows
-  // beside them) of U tokens at a time, so that all its reads of the other
-  // CTAs are in flight together (one such read takes about 500 clocks).
+  // beside them) of U tokens at a time.
   constexpr int LANES = GATED ? 16 : 32, GROUPS = 256 / LANES, U = GATED ? 2 : 4;
-  const int share = (BN + S - 1) / S;
-  const int last = min(min(BN, (rank + 1) * share), args.tokens - tt * BN);
+  const int last = min(share, tokens - rank * share);  // this CTA's tokens
   const int sub = threadIdx.x % LANES;
   const int col = wt * (GATED ? 64 : 128) + sub * 4;
-  int t0 = rank * share + static_cast<int>(threadIdx.x) / LANES;
+  int t0 = static_cast<int>(threadIdx.x) / LANES;
   if (warp >= 8 || col >= args.rows) t0 = last;
   for (; t0 < last; t0 += U * GROUPS) {
-    const uint32_t base = smem_u32(smem) + sub * 16;
+    const uint32_t base = copies + sub * 16;
     float4 v[U], u[GATED ? U : 1];
 #pragma unroll
     for (int k = 0; k < U; ++k) {
       v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (GATED) u[k] = v[k];
     }
-    if (S == 1) {
+#pragma unroll 2
+    for (int p = 0; p < S; ++p) {
 #pragma unroll
       for (int k = 0; k < U; ++k) {  // past the end: the last token again, not stored
-        const uint32_t at = base + min(t0 + k * GROUPS, BN - 1) * 512;
-        v[k] = ld_shared_f4(at);
-        if (GATED) u[k] = ld_shared_f4(at + 256);
-      }
-    } else {
-#pragma unroll 4
-      for (int p = 0; p < S; ++p) {
-        const uint32_t from = map_rank(base, p);
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-          const uint32_t at = from + min(t0 + k * GROUPS, BN - 1) * 512;
-          add4(v[k], ld_cluster_f4(at));
-          if (GATED) add4(u[k], ld_cluster_f4(at + 256));
-        }
+        const uint32_t at = base + (p * share + min(t0 + k * GROUPS, last - 1)) * 512;
+        add4(v[k], ld_shared_f4(at));
+        if (GATED) add4(u[k], ld_shared_f4(at + 256));
       }
     }
 #pragma unroll
     for (int k = 0; k < U; ++k) {
       const int t = t0 + k * GROUPS;
-      const int64_t token = static_cast<int64_t>(tt) * BN + t;
+      const int64_t token = static_cast<int64_t>(tt) * BN + rank * share + t;
       if (t < last) {
         const int64_t at = token * args.rows + col;
         if (GATED) {
@@ -294,7 +308,6 @@ __global__ void __launch_bounds__(THREADS)
       }
     }
   }
-  if (S > 1) cluster_sync();  // the others may still be reading this CTA's copy
   if (*abort_flag) {
     // give bulk copies already in flight time to land before the CTA ends
     for (int i = 0; i < 1000; ++i) __nanosleep(1000);
@@ -313,7 +326,9 @@ cudaError_t launch(const CUtensorMap (&tm)[4], const NarrowArgs& a, int stages, 
   if (cudaError_t e = ff_all_smem(k_narrow<F8, W_MN, BN, OUT>, ready)) return e;
   count_launch();
   return ff_launch(k_narrow<F8, W_MN, BN, OUT>, static_cast<int64_t>(tiles) * S, THREADS,
-                   stages * (W_BYTES + BN * 128 + (F8 ? SCALES : 0)) + 1024 + 512, S, s, tm[0],
+                   stages * (W_BYTES + BN * 128 + (F8 ? SCALES : 0)) + 1024 + 512 +
+                       (S > 1 ? (BN + S) * 512 : 0),
+                   S, s, tm[0],
                    tm[1], tm[2], tm[3], a, stages, S);
 }
 
@@ -358,12 +373,14 @@ bool ff_narrow_product(const FfProduct& p, cudaStream_t s, cudaError_t* err) {
   a.per = (a.kblocks + plan.split - 1) / plan.split;
   const int tiles = plan.tiles, S = plan.split;
   const int stage = W_BYTES + bn * 128 + (p.f8 ? SCALES : 0);
-  // up to 64 tokens half an SM's shared memory, so that two CTAs are resident,
-  // of this launch or of the next one
-  int stages = ((bn <= 64 ? 112 : 224) * 1024 - 1536) / stage;
-  if (stages > a.per && a.per * stage >= bn * 512) stages = a.per;
-  // the accumulator's copy (512 bytes per token) reuses the stages
-  while (stages * stage < bn * 512) ++stages;
+  // up to 32 tokens, and where two CTAs per SM are wanted, half an SM's shared
+  // memory: two CTAs are resident, of this launch or of the next one
+  const int extra = 1024 + 512 + (S > 1 ? (bn + S) * 512 : 0);
+  int stages = ((bn <= 32 || plan.two ? 112 : 224) * 1024 - extra) / stage;
+  if (stages > 12) stages = 12;
+  if (stages > a.per) stages = a.per;
+  // with S = 1 the accumulator's copy (512 bytes per token) takes their place
+  while (S == 1 && stages * stage < bn * 512) ++stages;
 #define ALX_NARROW(F8_, MN_, OUT_, BN_)                                              \
   if (p.f8 == F8_ && p.b_mn == MN_ && p.out_kind == OUT_ && bn == BN_) {              \
     *err = launch<F8_, MN_, BN_, OUT_>(tm, a, stages, S, tiles, s);                   \
@@ -384,7 +401,7 @@ bool ff_narrow_product(const FfProduct& p, cudaStream_t s, cudaError_t* err) {
 
 // What a narrow product costs, in ns, fitted to a B200 (back to back, rows 512
 // to 18432, K 512 to 18432 elements, 1 to 2048 tokens): 5.5 us of first loads
-// and epilogue, 1 us and 16 ns per token of the tile more to join a cluster;
+// and epilogue, 0.6 us and 8 ns per token of the tile more to join a cluster;
 // then the slowest of reading the weights (6.3 TB/s, 5.5 with about one CTA per
 // SM, at most 45 GB/s per CTA), moving all operands into the SMs (12 TB/s), and
 // the steps of K that one SM walks (0.27 us each); a second wave of CTAs starts
@@ -402,6 +419,7 @@ FfNarrowPlan ff_narrow_plan(int tokens, int rows, int kblocks) {
   p.bn = bn;
   p.tiles = ((rows + 127) / 128) * ((tokens + bn - 1) / bn);
   p.split = 1;
+  p.two = false;
   p.ns = 0;
   const double weights = 128.0 * rows * kblocks;
   const double moved = 128.0 * (128 + bn) * p.tiles * kblocks;
@@ -419,10 +437,11 @@ FfNarrowPlan ff_narrow_plan(int tokens, int rows, int kblocks) {
     double t = weights / rate;
     if (moved / 12000 > t) t = moved / 12000;
     if (waves * per * 270 > t) t = waves * per * 270;
-    t += 5500 + (S > 1 ? 1000 + 16 * bn : 0) + (two ? 0 : 4500 * (waves - 1));
+    t += 5500 + (S > 1 ? 600 + 8 * bn : 0) + (two ? 0 : 4500 * (waves - 1));
     if (p.ns == 0 || t <= p.ns) {
       p.ns = t;
       p.split = S;
+      p.two = two;
     }
   }
   return p;
