@@ -50,6 +50,7 @@ struct PairArgs {
   int fresh;             // clear the status word first
   int beside;            // independent of the launch before it: wait for that at the end
   int rounds, early;     // tile_of
+  int band;              // tile_at
   uint32_t idesc;
   void* out;
   GateSave save;
@@ -67,16 +68,15 @@ __device__ __forceinline__ int tile_of(const PairArgs& a, int total, int i, int 
   return t < total ? t : -1;
 }
 
-// Tiles in bands of 8 rows of tiles, column by column inside a band: the
+// Tiles in bands of `band` rows of tiles, column by column inside a band: the
 // tiles that run at one time then share few rows of A and B, which stay in L2.
 __device__ __forceinline__ void tile_at(const PairArgs& a, int t, int& m, int& n) {
-  constexpr int BAND = 8;
-  const int per_band = BAND * a.n_tiles;
+  const int per_band = a.band * a.n_tiles;
   const int band = t / per_band;
-  const int rows = min(BAND, a.m_tiles - band * BAND);
+  const int rows = min(a.band, a.m_tiles - band * a.band);
   const int r = t - band * per_band;
   n = r / rows;
-  m = band * BAND + (r - n * rows);
+  m = band * a.band + (r - n * rows);
 }
 
 // 16 columns of this warp's 32 lanes, not yet waited for.
@@ -527,6 +527,12 @@ bool ff_pair_product(const FfProduct& p, cudaStream_t s, cudaError_t* err) {
   const int pairs = ff_num_sms() / 2;
   const int tiles = a.m_tiles * a.n_tiles;
   const int grid = 2 * (tiles < pairs ? tiles : pairs);
+  // One band where all of A stays in L2 (40 MB of its 126), so that B passes by
+  // once: 4096 rows of 4096 in bf16 465 -> 455 us, 8192 in 8 bits 277 -> 268;
+  // else eight rows of tiles (16 instead cost the data and weight gradients
+  // 1%).
+  const int64_t row_tile = static_cast<int64_t>(a.kblocks) * 256 * 128;
+  a.band = a.m_tiles * row_tile <= (40ll << 20) ? a.m_tiles : 8;
   a.rounds = 0x7FFFFFFF;
   a.early = pairs;
   a.beside = p.beside_tiles > 0;
