@@ -12,7 +12,9 @@ using namespace alx;
 
 namespace {
 
-constexpr int MAX_DIM = 1 << 24;  // columns of any matrix here: keeps 2F and tile counts in an int
+// columns and rows of any matrix here: keeps 2F, tile counts and the tiles'
+// coordinates in an int
+constexpr int MAX_DIM = 1 << 24, MAX_ROWS = 1 << 30;
 
 size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 alexnet_status done(cudaError_t e) { return e == cudaSuccess ? ALEXNET_OK : ALEXNET_ERR_CUDA; }
@@ -127,7 +129,9 @@ alexnet_status alexnet_op_rmsnorm_bwd(const void* dy, const void* dsum, const vo
 }
 
 size_t alexnet_fc_f8_workspace_bytes(int B, int In, int Out) {
-  if (B < 1 || In < 1 || Out < 1 || In % 16 || Out % 8 || In > MAX_DIM || Out > MAX_DIM) return 0;
+  if (B < 1 || In < 1 || Out < 1 || In % 16 || Out % 8 || In > MAX_DIM || Out > MAX_DIM ||
+      B > MAX_ROWS)
+    return 0;
   return 256;
 }
 
@@ -139,7 +143,7 @@ alexnet_status alexnet_op_fc_f8_fwd(const void* x, const uint8_t* xs, int x_fmt,
       bad_fmt(x_fmt) || bad_fmt(w_fmt) || bad_dtype(y_dtype) ||
       bad16(x, xs, w, wscales, y, ws))
     return ALEXNET_ERR_INVALID_ARG;
-  if (In > MAX_DIM || Out > MAX_DIM) return ALEXNET_ERR_UNSUPPORTED;
+  if (In > MAX_DIM || Out > MAX_DIM || B > MAX_ROWS) return ALEXNET_ERR_UNSUPPORTED;
   if (!ws || ws_bytes < alexnet_fc_f8_workspace_bytes(B, In, Out)) return ALEXNET_ERR_INVALID_ARG;
   FfProduct p;
   memset(&p, 0, sizeof(p));
@@ -155,7 +159,7 @@ alexnet_status alexnet_op_fc_f8_fwd(const void* x, const uint8_t* xs, int x_fmt,
 }
 
 size_t alexnet_gated_workspace_bytes(int B, int In, int F) {
-  if (!gated_dims(B, In, F, 8) || In > MAX_DIM || F > MAX_DIM) return 0;
+  if (!gated_dims(B, In, F, 8) || In > MAX_DIM || F > MAX_DIM || B > MAX_ROWS) return 0;
   return 256 + up256(8ull * B * F) + up256(2ull * B * In);
 }
 
@@ -230,7 +234,7 @@ alexnet_status alexnet_op_gated_fwd(const void* x, int B, int In, const void* w,
   if (!x || !w || !h || !gated_dims(B, In, F, 8) || bad_act(act) || bad_dtype(gu_dtype) ||
       bad16(x, w, h, gu, ws))
     return ALEXNET_ERR_INVALID_ARG;
-  if (In > MAX_DIM || F > MAX_DIM) return ALEXNET_ERR_UNSUPPORTED;
+  if (In > MAX_DIM || F > MAX_DIM || B > MAX_ROWS) return ALEXNET_ERR_UNSUPPORTED;
   if (!ws || ws_bytes < alexnet_gated_workspace_bytes(B, In, F)) return ALEXNET_ERR_INVALID_ARG;
   return gated_fwd(x, B, In, w, F, act, h, save_of(gu_dtype, gu), ws, cu(stream));
 }
@@ -241,7 +245,7 @@ alexnet_status alexnet_op_gated_fwd_ckpt8(const void* x, int B, int In, const vo
   if (!x || !w || !h || !guq || !gus || !gated_dims(B, In, F, 16) || bad_act(act) ||
       bad16(x, w, h, guq, gus, ws))
     return ALEXNET_ERR_INVALID_ARG;
-  if (In > MAX_DIM || F > MAX_DIM) return ALEXNET_ERR_UNSUPPORTED;
+  if (In > MAX_DIM || F > MAX_DIM || B > MAX_ROWS) return ALEXNET_ERR_UNSUPPORTED;
   if (!ws || ws_bytes < alexnet_gated_workspace_bytes(B, In, F)) return ALEXNET_ERR_INVALID_ARG;
   return gated_fwd(x, B, In, w, F, act, h, save_of(guq, gus), ws, cu(stream));
 }
@@ -252,7 +256,7 @@ alexnet_status alexnet_op_gated_bwd(const void* dh, const void* x, int gu_dtype,
   if (!dh || !x || !gu || !w || !gated_dims(B, In, F, 8) || bad_act(act) || bad_dtype(gu_dtype) ||
       bad16(dh, x, gu, w, dx, dw, ws))
     return ALEXNET_ERR_INVALID_ARG;
-  if (In > MAX_DIM || F > MAX_DIM) return ALEXNET_ERR_UNSUPPORTED;
+  if (In > MAX_DIM || F > MAX_DIM || B > MAX_ROWS) return ALEXNET_ERR_UNSUPPORTED;
   if (!ws || ws_bytes < alexnet_gated_workspace_bytes(B, In, F)) return ALEXNET_ERR_INVALID_ARG;
   return gated_bwd(dh, x, save_of(gu_dtype, gu), B, In, w, F, act, dx, dw, ws, cu(stream));
 }
@@ -264,7 +268,7 @@ alexnet_status alexnet_op_gated_bwd_ckpt8(const void* dh, const void* xq, const 
   if (!dh || !xq || !xs || !guq || !gus || !w || !gated_dims(B, In, F, 16) || bad_act(act) ||
       bad16(dh, xq, xs, guq, gus, w, dx, dw, ws))
     return ALEXNET_ERR_INVALID_ARG;
-  if (In > MAX_DIM || F > MAX_DIM) return ALEXNET_ERR_UNSUPPORTED;
+  if (In > MAX_DIM || F > MAX_DIM || B > MAX_ROWS) return ALEXNET_ERR_UNSUPPORTED;
   if (!ws || ws_bytes < alexnet_gated_workspace_bytes(B, In, F)) return ALEXNET_ERR_INVALID_ARG;
   GateSave save = save_of(guq, gus);
   bf16* xb = reinterpret_cast<bf16*>(U8(ws) + 256 + up256(8ull * B * F));

@@ -237,7 +237,8 @@ ALEXNET_API alexnet_status alexnet_op_rmsnorm_bwd(const void* dy, const void* ds
  *   y[b,o] = sum_i x[b,i] w[o,i]
  * x 8-bit rows [B, In] of type x_fmt with scales xs, w 8-bit rows [Out, In]
  * of type w_fmt with scales wscales; y [B, Out] in y_dtype (alexnet_dtype).
- * In % 16 == 0, Out % 8 == 0. */
+ * In % 16 == 0, Out % 8 == 0 (for these and the gated block: columns up to
+ * 2^24 and B up to 2^30, else UNSUPPORTED). */
 ALEXNET_API size_t alexnet_fc_f8_workspace_bytes(int B, int In, int Out);
 ALEXNET_API alexnet_status alexnet_op_fc_f8_fwd(const void* x, const uint8_t* xs, int x_fmt, int B,
                                                 int In, const void* w, const uint8_t* wscales,

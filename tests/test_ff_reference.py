@@ -86,10 +86,10 @@ def test_sizes(ax):
     for r, c in ((0, 8), (1, 12), (1, 65544), (1 << 31, 8)):
         assert ax.rmsnorm_workspace_bytes(r, c) == 0
     assert ax.fc_f8_workspace_bytes(1, 16, 8) > 0
-    for s in ((0, 16, 8), (1, 24, 8), (1, 16, 12), (1, 0, 8), (1, 1 << 25, 8)):
+    for s in ((0, 16, 8), (1, 24, 8), (1, 16, 12), (1, 0, 8), (1, 1 << 25, 8), ((1 << 30) + 1, 16, 8)):
         assert ax.fc_f8_workspace_bytes(*s) == 0
     assert ax.gated_workspace_bytes(1, 8, 8) > 0
-    for s in ((0, 8, 8), (1, 12, 8), (1, 8, 12), (1, 1 << 25, 8), (1, 8, 1 << 25)):
+    for s in ((0, 8, 8), (1, 12, 8), (1, 8, 12), (1, 1 << 25, 8), (1, 8, 1 << 25), ((1 << 30) + 1, 8, 8)):
         assert ax.gated_workspace_bytes(*s) == 0
 
 
@@ -121,7 +121,7 @@ def test_refusals(ax):
     _refused(ax, "alexnet_op_fc_f8_fwd", [P, P, 0, 4, 32, P, P, 1, 8, 1, P, P, BIG, None],
              [(0, None), (0, P + 8), (1, None), (1, P + 8), (2, 2), (3, 0), (4, 24), (4, 0), (5, None), (5, P + 8), (6, None), (6, P + 8),
               (7, -1), (8, 12), (8, 0), (9, 2), (10, None), (10, P + 8), (11, None), (11, P + 8), (12, 0)],
-             [(4, 1 << 25), (8, 1 << 25)])
+             [(3, (1 << 30) + 1), (4, 1 << 25), (8, 1 << 25)])
     _refused(ax, "alexnet_op_gated_fwd", [P, 4, 16, P, 8, 0, P, 1, P, P, BIG, None],
              [(0, None), (0, P + 8), (1, 0), (2, 12), (2, 0), (3, None), (3, P + 8), (4, 12), (4, 0), (5, 3), (5, -1), (6, None), (6, P + 8),
               (7, 2), (8, P + 8), (9, None), (9, P + 8), (10, 0)],
@@ -129,7 +129,7 @@ def test_refusals(ax):
     _refused(ax, "alexnet_op_gated_bwd", [P, P, 0, P, 4, 16, P, 8, 0, P, P, P, BIG, None],
              [(0, None), (0, P + 8), (1, None), (1, P + 8), (2, -1), (3, None), (3, P + 8), (4, 0), (5, 12), (6, None), (7, 12), (8, 3),
               (9, P + 8), (10, P + 8), (11, None), (11, P + 8), (12, 0)],
-             [(5, 1 << 25), (7, 1 << 25)])
+             [(4, (1 << 30) + 1), (5, 1 << 25), (7, 1 << 25)])
     _refused(ax, "alexnet_op_gated_fwd_ckpt8", [P, 4, 16, P, 16, 0, P, P, P, P, BIG, None],
              [(0, None), (1, 0), (2, 24), (3, None), (4, 24), (5, 3), (6, None), (7, None), (7, P + 8), (8, None), (8, P + 8), (9, None),
               (10, 0)],

@@ -428,23 +428,57 @@ def test_gated_large_projections(ax, kind):
     within(dw, ww, ew)
 
 
-@pytest.mark.parametrize("B", [4, 150])
-def test_gated_lost_values_stay_in_their_row(ax, B):
+@pytest.mark.parametrize("kind", [0, 1, 2])
+@pytest.mark.parametrize("B", [4, 150, 600])
+def test_gated_lost_values_stay_in_their_row(ax, B, kind):
     import torch
     In, F = 136, 200
     x, w, dh = _gated_in(B, In, F)
     ws = work(ax.gated_workspace_bytes(B, In, F))
     h, gu, dx, dw = out((B, F)), out((B, 2 * F)), out((B, In)), out((2 * F, In))
-    ax.op_gated_fwd(x, B, In, w, F, 0, h, ax.BF16, gu, ws)
-    ax.op_gated_bwd(dh, x, ax.BF16, gu, B, In, w, F, 0, dx, dw, ws)
+    ax.op_gated_fwd(x, B, In, w, F, kind, h, ax.BF16, gu, ws)
+    ax.op_gated_bwd(dh, x, ax.BF16, gu, B, In, w, F, kind, dx, dw, ws)
     clean, cleanx = h.clone(), dx.clone()
     x[2, 135] = float("nan")
     x[B - 1, 0] = float("inf")
-    ax.op_gated_fwd(x, B, In, w, F, 0, h, ax.BF16, gu, ws)
-    ax.op_gated_bwd(dh, x, ax.BF16, gu, B, In, w, F, 0, dx, None, ws)
+    ax.op_gated_fwd(x, B, In, w, F, kind, h, ax.BF16, gu, ws)
+    ax.op_gated_bwd(dh, x, ax.BF16, gu, B, In, w, F, kind, dx, None, ws)
     keep = [i for i in range(B) if i not in (2, B - 1)]
     assert torch.equal(h[keep], clean[keep]) and torch.equal(dx[keep], cleanx[keep])
-    assert bool(torch.isnan(h[2]).all()) and not bool(torch.isfinite(h[B - 1]).any())
+    assert bool(torch.isnan(h[2]).all()) and bool(torch.isnan(dx[2]).all())
+    # +-inf * +-inf of the projections, or a gate of -inf: never a finite value
+    # but for relu's gates at -inf, which are 0 * inf = NaN
+    assert not bool(torch.isfinite(h[B - 1]).any())
+
+
+@pytest.mark.parametrize("B", [3, 200])
+def test_ckpt8_lost_values_stay_in_their_row(ax, B):
+    """A NaN or an infinity in one row's projections: NaN codes there, nothing
+    in the other rows' codes, scales and gradients."""
+    import torch
+    In, F = 144, 272
+    x, w, dh = _gated_in(B, In, F)
+    ws = work(ax.gated_workspace_bytes(B, In, F))
+    n = ax.f8_scale_bytes(B, F)
+    h, guq, gus, dx = out((B, F)), out((2, B, F), "uint8"), out((2, n), "uint8"), out((B, In))
+    xq, xs = out((B, In), "uint8"), out((ax.f8_scale_bytes(B, In),), "uint8")
+
+    def go():
+        ax.op_f8_quant(x, B, In, ax.E4M3, xq, xs)
+        ax.op_gated_fwd_ckpt8(x, B, In, w, F, 0, h, guq, gus, ws)
+        ax.op_gated_bwd_ckpt8(dh, xq, xs, guq, gus, B, In, w, F, 0, dx, None, ws)
+        return [t.clone() for t in (h, guq, gus, dx)]
+
+    clean = go()
+    x[1, 7], x[2, 9] = float("nan"), float("inf")
+    bad = go()
+    keep = [i for i in range(B) if i not in (1, 2)]
+    assert torch.equal(bad[0][keep], clean[0][keep]) and torch.equal(bad[3][keep], clean[3][keep])
+    assert torch.equal(bad[1][:, keep], clean[1][:, keep])
+    at = ff.tile_index(B, F, "cuda")[keep].flatten()
+    assert torch.equal(bad[2][:, at], clean[2][:, at])
+    assert bool(torch.isnan(ff.code_values(bad[1][:, [1, 2]])).all())
+    assert bool(torch.isnan(bad[3][[1, 2]]).all())
 
 
 def test_gated_gradient_against_differences(ax):
