@@ -20,6 +20,13 @@
 //
 // Roles (320 threads): warps 0-7 epilogue, warp 8 TMA producer, warp 9 MMA
 // issuer and TMEM owner.
+//
+// Measured (calls back to back, weights from DRAM): gated block 4096 -> 9216
+// with one token 25.5 us (151 MB of weights: 5.9 TB/s), 8-bit 4096 -> 9216 with
+// one token 9.9 us (37.7 MB), 8-bit 9216 -> 4096 with 128 tokens 13.7 us.  What
+// is left beside the streaming (23, 5.8 and 6.5 us) is the way in and out: about
+// 1.5 us from the end of the kernel before to the first operands, 1 to 2 us
+// from the last product to the end, 1 us between two grids.
 #include <cstring>
 
 #include "f8.cuh"

@@ -71,8 +71,8 @@ __device__ __forceinline__ uint2 codes8(const float (&f)[8], float inv, int e5m2
 // block) hold it in registers as bf16, NV vectors of 8 columns each (thread t
 // the vectors t, t + G, ...), so the rounded s is also what the statistic and
 // the gradient see.  16 neighbouring lanes hold one 128-column block of the
-// 8-bit output.  Bound by its bytes (x, res, s, codes: 7 per column): 6.1 TB/s,
-// 0.93 of a copy, at 8192 x 4096.
+// 8-bit output.  Bound by its bytes (x, res, s, codes: 7 per column): 39 us at
+// 8192 x 4096, 6.0 TB/s, 0.91 of a copy.
 template <int NV, bool BLOCK>
 __global__ void __launch_bounds__(NV > 4 ? 1024 : 512)
     k_rmsnorm_fwd(const bf16* x, const bf16* res, const float* __restrict__ gamma, int64_t rows,
@@ -207,9 +207,12 @@ __device__ __forceinline__ void put_acc(const float (&acc)[NV][8], int t, int G,
 // of this block ahead.  A block walks rows blockIdx.x, blockIdx.x + gridDim.x,
 // ...; a thread's columns are the same in all of them, so the sums of dy s rstd
 // stay in registers and each block writes one row of `parts` at its end.
-// Bound by its bytes (dy, s, dsum, dx: 8 per column).  Loads into registers one
-// row ahead instead took 107 registers, which leaves one block of nine warps
-// per SM (33 us at 4001 x 4112); at 96 the compiler gave up the look-ahead.
+// Bound by its bytes (dy, s, dsum, dx: 8 per column): 27 us at 4001 x 4112, 4.8
+// TB/s (47 us and 5.7 at 8192 x 4096), and 5 more for the sum of `parts`.
+// Loads into registers one row ahead instead took 107 registers, which leaves
+// one block of nine warps per SM (33 us); at 96 the compiler gave up the
+// look-ahead (31 us).  One vector per thread (NV = 1) instead of two halves a
+// row's way through the block: 29.4 -> 27.2 us.
 template <int NV>
 __global__ void __launch_bounds__(NV == 1 ? 1024 : 512)
     k_rmsnorm_bwd_staged(const bf16* dy, const bf16* dsum, const bf16* sum,
