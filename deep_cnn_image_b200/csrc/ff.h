@@ -74,18 +74,27 @@ struct GateSave {
   bf16* b16;      // [B, 2F]
   uint8_t* q;     // two 8-bit matrices [B, F], one after the other,
   uint8_t* qs;    // and their scales
-  // with q, for the backward: the block's input as 8-bit rows [B, In] and where
-  // its values go (null: not wanted)
+};
+// The block's input for the weight gradient: bf16, or 8-bit rows (x null).
+struct GateInput {
+  const bf16* x;
   const uint8_t *xq, *xs;
-  bf16* xb;
+  bf16* out;      // where the launch puts its values (null: nowhere)
   int In;
 };
+// Up to this many tokens the backward's dz is kept in two bf16 terms, whose sum
+// is exact to 2^-16: row 2b holds the rounded values of token b, row 2b + 1 what
+// the rounding left over, and the input's rows are doubled to match.  Its
+// products are bound by the weights there, not by their rows, and with few
+// tokens dz's rounding does not average out: at 8 tokens it made dx's error 1.5
+// times that of its own last rounding.
+constexpr int TWO_TERM_TOKENS = 64;
 // z fp32 [B, 2F] -> h, and z in what `save` holds
 cudaError_t launch_gate_fwd(const float* z, int B, int F, int act, bf16* h, const GateSave& save,
                             cudaStream_t s);
-// dz bf16 [B, 2F] from dh and the saved projections, and the saved input's
-// values; *status = 0
-cudaError_t launch_gate_bwd(const bf16* dh, const GateSave& save, int B, int F, int act, bf16* dz,
-                            int* status, cudaStream_t s);
+// dz bf16 [B, 2F] ([2B, 2F] in two terms) from dh and the saved projections, and
+// the input's values where they are wanted; *status = 0
+cudaError_t launch_gate_bwd(const bf16* dh, const GateSave& save, const GateInput& in, int B, int F,
+                            int act, bf16* dz, int* status, cudaStream_t s);
 
 }  // namespace alx

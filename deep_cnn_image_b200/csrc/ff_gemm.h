@@ -27,6 +27,9 @@ struct FfProduct {
   void* out;
   int act;
   GateSave save;
+  // narrow products of bf16 with b_mn only: rows 2i and 2i + 1 of A are two
+  // terms of one row, M counts both, and out has M / 2 rows
+  int fold;
   int* status;   // bit 0: a bounded wait ran out;
   int fresh;     // set it to 0 first
   // > 0: independent of the pair launch just before it in the stream, which has

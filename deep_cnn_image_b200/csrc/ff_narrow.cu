@@ -54,7 +54,7 @@ struct NarrowArgs {
   int token_tiles;
   int k_tiles;             // scale tiles per 128 rows
   int act;
-  int fresh;
+  int fresh, fold;
   uint32_t idesc;
   void* out;
   GateSave save;
@@ -136,7 +136,10 @@ __global__ void __launch_bounds__(THREADS)
   const uint32_t tmem_base = *tmem_slot;
   if (S > 1) cluster_arrive();  // this CTA runs: the others may write to it
   const int tokens = min(BN, args.tokens - tt * BN);  // of this tile
-  const int share = (BN + S - 1) / S;                 // of them per CTA
+  // with `fold` two rows of the activations make one token, and stay together
+  constexpr bool FOLDS = W_MN && OUT == FF_BF16;
+  const int terms = FOLDS && args.fold ? 2 : 1;
+  const int share = (BN / terms + S - 1) / S * terms;  // of them per CTA
   // where the partial sums go: S copies of [share][128], behind the barriers
   const uint32_t copies = S == 1 ? sW : bar_full + 256;
   grid_dep_launch();
@@ -269,7 +272,7 @@ __global__ void __launch_bounds__(THREADS)
   // A thread adds up four rows (gated: four gate rows and the four up rows
   // beside them) of U tokens at a time.
   constexpr int LANES = GATED ? 16 : 32, GROUPS = 256 / LANES, U = GATED ? 2 : 4;
-  const int last = min(share, tokens - rank * share);  // this CTA's tokens
+  const int last = min(share, tokens - rank * share) / terms;  // this CTA's results
   const int sub = threadIdx.x % LANES;
   const int col = wt * (GATED ? 64 : 128) + sub * 4;
   int t0 = static_cast<int>(threadIdx.x) / LANES;
@@ -286,15 +289,16 @@ __global__ void __launch_bounds__(THREADS)
     for (int p = 0; p < S; ++p) {
 #pragma unroll
       for (int k = 0; k < U; ++k) {  // past the end: the last token again, not stored
-        const uint32_t at = base + (p * share + min(t0 + k * GROUPS, last - 1)) * 512;
+        const uint32_t at = base + (p * share + min(t0 + k * GROUPS, last - 1) * terms) * 512;
         add4(v[k], ld_shared_f4(at));
+        if (FOLDS && terms == 2) add4(v[k], ld_shared_f4(at + 512));
         if (GATED) add4(u[k], ld_shared_f4(at + 256));
       }
     }
 #pragma unroll
     for (int k = 0; k < U; ++k) {
       const int t = t0 + k * GROUPS;
-      const int64_t token = static_cast<int64_t>(tt) * BN + rank * share + t;
+      const int64_t token = (static_cast<int64_t>(tt) * BN + rank * share) / terms + t;
       if (t < last) {
         const int64_t at = token * args.rows + col;
         if (GATED) {
@@ -334,7 +338,7 @@ cudaError_t launch(const CUtensorMap (&tm)[4], const NarrowArgs& a, int stages, 
   count_launch();
   return ff_launch(k_narrow<F8, W_MN, BN, OUT>, static_cast<int64_t>(tiles) * S, THREADS,
                    stages * (W_BYTES + BN * 128 + (F8 ? SCALES : 0)) + 1024 + 512 +
-                       (S > 1 ? (BN + S) * 512 : 0),
+                       (S > 1 ? (BN + 2 * S) * 512 : 0),
                    S, s, tm[0],
                    tm[1], tm[2], tm[3], a, stages, S);
 }
@@ -345,6 +349,7 @@ bool ff_narrow_product(const FfProduct& p, cudaStream_t s, cudaError_t* err) {
   // here the activations are p.a [tokens, K] and the weights p.b
   const bool gated = p.out_kind == FF_GATED;
   if (p.a_mn || (p.b_mn && (p.f8 || gated)) || p.save.q) return false;
+  if (p.fold && (!p.b_mn || p.out_kind != FF_BF16 || p.M > 128)) return false;
   const int K = p.f8 ? p.K / 2 : p.K;
   const int kblocks = (K + 63) / 64;
   const FfNarrowPlan plan = ff_narrow_plan(p.M, gated ? 2 * p.N : p.N, kblocks);
@@ -363,6 +368,7 @@ bool ff_narrow_product(const FfProduct& p, cudaStream_t s, cudaError_t* err) {
   a.token_tiles = (p.M + bn - 1) / bn;
   a.act = p.act;
   a.fresh = p.fresh;
+  a.fold = p.fold;
   a.out = p.out;
   a.save = p.save;
   a.status = p.status;
@@ -382,7 +388,7 @@ bool ff_narrow_product(const FfProduct& p, cudaStream_t s, cudaError_t* err) {
   const int stage = W_BYTES + bn * 128 + (p.f8 ? SCALES : 0);
   // up to 32 tokens, and where two CTAs per SM are wanted, half an SM's shared
   // memory: two CTAs are resident, of this launch or of the next one
-  const int extra = 1024 + 512 + (S > 1 ? (bn + S) * 512 : 0);
+  const int extra = 1024 + 512 + (S > 1 ? (bn + 2 * S) * 512 : 0);
   int stages = ((bn <= 32 || plan.two ? 112 : 224) * 1024 - extra) / stage;
   if (stages > 12) stages = 12;
   if (stages > a.per) stages = a.per;

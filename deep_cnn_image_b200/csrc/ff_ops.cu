@@ -42,6 +42,7 @@ bool gated_dims(int B, int In, int F, int step) {
 // 53; 8-bit product 9216 -> 4096 with 128 tokens 15 / 32, 512 tokens 29 / 32.
 bool runs_narrow(const FfProduct& p) {
   if (p.a_mn) return false;
+  if (p.fold) return true;
   const int rows = p.out_kind == FF_GATED ? 2 * p.N : p.N;
   const int kblocks = ((p.f8 ? p.K : 2 * p.K) + 127) / 128;
   // with 8-bit checkpoints the narrow kernel leaves gate and codes to a second
@@ -160,7 +161,7 @@ alexnet_status alexnet_op_fc_f8_fwd(const void* x, const uint8_t* xs, int x_fmt,
 
 size_t alexnet_gated_workspace_bytes(int B, int In, int F) {
   if (!gated_dims(B, In, F, 8) || In > MAX_DIM || F > MAX_DIM || B > MAX_ROWS) return 0;
-  return 256 + up256(8ull * B * F) + up256(2ull * B * In);
+  return 256 + up256(8ull * B * F) + up256((B <= TWO_TERM_TOKENS ? 4ull : 2ull) * B * In);
 }
 
 }  // extern "C"
@@ -206,15 +207,19 @@ alexnet_status gated_fwd(const void* x, int B, int In, const void* w, int F, int
   return product(p, s);
 }
 
-alexnet_status gated_bwd(const void* dh, const void* x, const GateSave& save, int B, int In,
+alexnet_status gated_bwd(const void* dh, GateInput in, const GateSave& save, int B, int In,
                          const void* w, int F, int act, void* dx, void* dw, void* ws,
                          cudaStream_t s) {
   bf16* dz = reinterpret_cast<bf16*>(U8(ws) + 256);
   int* status = static_cast<int*>(ws);
-  if (cudaError_t e = launch_gate_bwd(B16(dh), save, B, F, act, dz, status, s)) return done(e);
-  FfProduct d = bf16_product(dz, 1, x, 1, 2 * F, In, B, dw, status);
+  const bool two = B <= TWO_TERM_TOKENS;
+  const int rows = two ? 2 * B : B;
+  if (dw && (two || !in.x)) in.out = reinterpret_cast<bf16*>(U8(ws) + 256 + up256(8ull * B * F));
+  if (cudaError_t e = launch_gate_bwd(B16(dh), save, in, B, F, act, dz, status, s)) return done(e);
+  FfProduct d = bf16_product(dz, 1, in.out ? in.out : in.x, 1, 2 * F, In, rows, dw, status);
   if (dx) {
-    const FfProduct q = bf16_product(dz, 0, w, 1, B, In, 2 * F, dx, status);
+    FfProduct q = bf16_product(dz, 0, w, 1, rows, In, 2 * F, dx, status);
+    q.fold = two;
     if (alexnet_status e = product(q, s)) return e;
     if (!runs_narrow(q)) {
       d.beside_tiles = ((B + 255) / 256) * ((In + 255) / 256);
@@ -258,7 +263,8 @@ alexnet_status alexnet_op_gated_bwd(const void* dh, const void* x, int gu_dtype,
     return ALEXNET_ERR_INVALID_ARG;
   if (In > MAX_DIM || F > MAX_DIM || B > MAX_ROWS) return ALEXNET_ERR_UNSUPPORTED;
   if (!ws || ws_bytes < alexnet_gated_workspace_bytes(B, In, F)) return ALEXNET_ERR_INVALID_ARG;
-  return gated_bwd(dh, x, save_of(gu_dtype, gu), B, In, w, F, act, dx, dw, ws, cu(stream));
+  return gated_bwd(dh, GateInput{B16(x), nullptr, nullptr, nullptr, In}, save_of(gu_dtype, gu), B,
+                   In, w, F, act, dx, dw, ws, cu(stream));
 }
 
 alexnet_status alexnet_op_gated_bwd_ckpt8(const void* dh, const void* xq, const uint8_t* xs,
@@ -270,10 +276,8 @@ alexnet_status alexnet_op_gated_bwd_ckpt8(const void* dh, const void* xq, const 
     return ALEXNET_ERR_INVALID_ARG;
   if (In > MAX_DIM || F > MAX_DIM || B > MAX_ROWS) return ALEXNET_ERR_UNSUPPORTED;
   if (!ws || ws_bytes < alexnet_gated_workspace_bytes(B, In, F)) return ALEXNET_ERR_INVALID_ARG;
-  GateSave save = save_of(guq, gus);
-  bf16* xb = reinterpret_cast<bf16*>(U8(ws) + 256 + up256(8ull * B * F));
-  if (dw) save.xq = U8(xq), save.xs = xs, save.xb = xb, save.In = In;
-  return gated_bwd(dh, xb, save, B, In, w, F, act, dx, dw, ws, cu(stream));
+  return gated_bwd(dh, GateInput{nullptr, U8(xq), xs, nullptr, In}, save_of(guq, gus), B, In, w, F,
+                   act, dx, dw, ws, cu(stream));
 }
 
 }  // extern "C"

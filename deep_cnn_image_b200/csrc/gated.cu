@@ -82,14 +82,21 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// dg = dh u a'(g), du = dh a(g) (and, with 8-bit checkpoints, the expansion of
-// the saved input); 8 columns per thread, the projections from
+// What rounding z to r left over; nothing where z is not finite (r carries it).
+__device__ __forceinline__ float left_over(float z, float r) {
+  const float l = z - r;
+  return fabsf(l) <= 3.402823466e38f ? l : 0.f;
+}
+
+// dg = dh u a'(g), du = dh a(g), rounded to one bf16 term or (TWO) two; and, for
+// the weight gradient, the input's values where they are not in memory as it
+// reads them (8-bit rows, doubled rows).  8 columns per thread, the projections from
 // bf16 (KIND 0), 8-bit rows (1) or fp32 (2).  Bound by its bytes: 6, 4 or 10
 // read and 4 written per element of h.
-template <int KIND>
+template <int KIND, int TWO>
 __global__ void __launch_bounds__(256)
-    k_gate_bwd(const bf16* __restrict__ dh, const GateSave save, int B, int F, int act,
-               bf16* __restrict__ dz, int* status) {
+    k_gate_bwd(const bf16* __restrict__ dh, const GateSave save, const GateInput input, int B,
+               int F, int act, bf16* __restrict__ dz, int* status) {
   grid_dep_launch();
   grid_dep_wait();
   if (blockIdx.x == 0 && threadIdx.x == 0) *status = 0;
@@ -131,31 +138,64 @@ __global__ void __launch_bounds__(256)
                      p[k]);
       }
     }
-    uint32_t og[4], ou[4];
+    float zg[8], zu[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float a0, e0, a1, e1;
-      gate_both(p[0][2 * j], act, a0, e0);
-      gate_both(p[0][2 * j + 1], act, a1, e1);
-      og[j] = pack_bf16(d[2 * j] * p[1][2 * j] * e0, d[2 * j + 1] * p[1][2 * j + 1] * e1);
-      ou[j] = pack_bf16(d[2 * j] * a0, d[2 * j + 1] * a1);
+    for (int j = 0; j < 8; ++j) {
+      float a, e;
+      gate_both(p[0][j], act, a, e);
+      zg[j] = d[j] * p[1][j] * e;
+      zu[j] = d[j] * a;
     }
-    bf16* o = dz + row * 2 * F + col;
-    *reinterpret_cast<uint4*>(o) = make_uint4(og[0], og[1], og[2], og[3]);
-    *reinterpret_cast<uint4*>(o + F) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
+    bf16* o = dz + row * (TWO ? 4 : 2) * F + col;
+#pragma unroll
+    for (int k = 0; k <= TWO; ++k) {
+      uint32_t og[4], ou[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        og[j] = pack_bf16(zg[2 * j], zg[2 * j + 1]);
+        ou[j] = pack_bf16(zu[2 * j], zu[2 * j + 1]);
+      }
+      *reinterpret_cast<uint4*>(o + k * 2 * static_cast<int64_t>(F)) =
+          make_uint4(og[0], og[1], og[2], og[3]);
+      *reinterpret_cast<uint4*>(o + k * 2 * static_cast<int64_t>(F) + F) =
+          make_uint4(ou[0], ou[1], ou[2], ou[3]);
+      if (TWO) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          zg[2 * j] = left_over(zg[2 * j], bf16_lo(og[j]));
+          zg[2 * j + 1] = left_over(zg[2 * j + 1], bf16_hi(og[j]));
+          zu[2 * j] = left_over(zu[2 * j], bf16_lo(ou[j]));
+          zu[2 * j + 1] = left_over(zu[2 * j + 1], bf16_hi(ou[j]));
+        }
+      }
+    }
   }
-  if (KIND == 1 && save.xb) {
-    // the same launch expands the saved input for the weight gradient
-    const int In = save.In, xvecs = In >> 4;
+  const int In = input.In;
+  if (KIND != 1 && input.out) {
+    const int xvecs = In >> 3;
+    const int64_t xtotal = static_cast<int64_t>(B) * xvecs;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < xtotal;
+         i += static_cast<int64_t>(gridDim.x) * 256) {
+      const int64_t row = i / xvecs;
+      const uint4 v = *reinterpret_cast<const uint4*>(input.x + i * 8);
+      bf16* o = input.out + (i + row * (TWO ? xvecs : 0)) * 8;
+      *reinterpret_cast<uint4*>(o) = v;
+      if (TWO) *reinterpret_cast<uint4*>(o + In) = v;
+    }
+  }
+  if (KIND == 1 && input.out) {
+    const int xvecs = In >> 4;
     const int x_tiles = (In + F8_TILE_COLS - 1) / F8_TILE_COLS;
     const int64_t xtotal = static_cast<int64_t>(B) * xvecs;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < xtotal;
          i += static_cast<int64_t>(gridDim.x) * 256) {
       const int64_t row = i / xvecs;
       const int c = static_cast<int>(i - row * xvecs);
-      const uint4 w = *reinterpret_cast<const uint4*>(save.xq + i * 16);
-      f8_expand16(w, f8_scale_val(save.xs[f8_scale_at(row, c >> 3, x_tiles)]), 0,
-                  save.xb + i * 16);
+      const uint4 w = *reinterpret_cast<const uint4*>(input.xq + i * 16);
+      const float sc = f8_scale_val(input.xs[f8_scale_at(row, c >> 3, x_tiles)]);
+      bf16* o = input.out + (i + row * (TWO ? xvecs : 0)) * 16;
+      f8_expand16(w, sc, 0, o);
+      if (TWO) f8_expand16(w, sc, 0, o + In);
     }
   }
 }
@@ -174,12 +214,14 @@ cudaError_t launch_gate_fwd(const float* z, int B, int F, int act, bf16* h, cons
   return ff_launch(k_gate_fwd, grid_for((blocks + 15) / 16), 256, 0, 0, s, z, B, F, act, h, save);
 }
 
-cudaError_t launch_gate_bwd(const bf16* dh, const GateSave& save, int B, int F, int act, bf16* dz,
-                            int* status, cudaStream_t s) {
+cudaError_t launch_gate_bwd(const bf16* dh, const GateSave& save, const GateInput& in, int B, int F,
+                            int act, bf16* dz, int* status, cudaStream_t s) {
   const int grid = grid_for((static_cast<int64_t>(B) * (F >> 3) + 255) / 256);
   count_launch();
-  return ff_launch(save.b16 ? k_gate_bwd<0> : (save.q ? k_gate_bwd<1> : k_gate_bwd<2>), grid, 256,
-                   0, 0, s, dh, save, B, F, act, dz, status);
+  auto* one = save.b16 ? k_gate_bwd<0, 0> : (save.q ? k_gate_bwd<1, 0> : k_gate_bwd<2, 0>);
+  auto* two = save.b16 ? k_gate_bwd<0, 1> : (save.q ? k_gate_bwd<1, 1> : k_gate_bwd<2, 1>);
+  return ff_launch(B <= TWO_TERM_TOKENS ? two : one, grid, 256, 0, 0, s, dh, save, in, B, F, act,
+                   dz, status);
 }
 
 }  // namespace alx
