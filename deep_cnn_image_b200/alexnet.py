@@ -138,11 +138,21 @@ def _ptr(t):
     return t if t is None or t.__class__ is int else t.data_ptr()
 
 
+def _current_stream():
+    """torch's current stream of the current device, as a handle (a Stream
+    object, as torch.cuda.current_stream() builds it, costs 3 us a call)."""
+    global _current_stream
+    from torch import _C
+    device, raw = _C._cuda_getDevice, _C._cuda_getCurrentRawStream
+
+    def _current_stream():
+        return raw(device())
+    return _current_stream()
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        # the handle alone: current_stream() builds a Stream object, 3 us a call
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -312,7 +322,8 @@ class AlexNet:
 
 # -- single-op entry points (alexnet_ops.h), same names ------------------------
 def _op(name, *args):
-    return check(getattr(lib, name)(*args))
+    status = getattr(lib, name)(*args)
+    return check(status) if status else status
 
 
 def op_conv_fwd(x, B, H, W, Cin, w, bias, Cout, K, pad, groups, relu, y, ws, stream=None):

@@ -84,8 +84,14 @@ __device__ __forceinline__ void f8_expand16(const uint4& w, float sc, int e5m2,
     o[2 * n] = pack_bf16(v[0] * sc, v[1] * sc);
     o[2 * n + 1] = pack_bf16(v[2] * sc, v[3] * sc);
   }
-  reinterpret_cast<uint4*>(out)[0] = make_uint4(o[0], o[1], o[2], o[3]);
-  reinterpret_cast<uint4*>(out)[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  if (reinterpret_cast<uintptr_t>(out) & 16) {
+    reinterpret_cast<uint4*>(out)[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    reinterpret_cast<uint4*>(out)[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  } else {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(out), "r"(o[0]),
+                 "r"(o[1]), "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
+                 : "memory");
+  }
 }
 
 }  // namespace alx

@@ -150,55 +150,99 @@ __global__ void __launch_bounds__(NV > 4 ? 1024 : 512)
 
 // dx = rstd (t - s rstd^2 mean(t s)) + dsum, t = dy gamma.
 //
+// Two fp32 values in one register pair: the packed multiply and fused
+// multiply-add do both at once (the wide kernels below spend more on issuing
+// instructions than on waiting for memory).
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ F2 f2_bf16(uint32_t u) { return f2(bf16_lo(u), bf16_hi(u)); }
+__device__ __forceinline__ float2 f2_get(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+  return r;
+}
+__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) {
+  return i == 0 ? v.x : (i == 1 ? v.y : (i == 2 ? v.z : v.w));
+}
+// gamma of vector u, zeros past the row's end
+__device__ __forceinline__ void load_gamma(const float* __restrict__ gamma, int u, int nvec,
+                                           F2 (&g)[4]) {
+  float a[8] = {};
+  if (u < nvec) load8(gamma + 8 * u, a);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) g[i] = f2(a[2 * i], a[2 * i + 1]);
+}
+
 // One row's part of it, for the threads that hold the row in registers (NV
-// vectors of dy, s and dsum each): adds dy s rstd to acc and stores dx.
-template <int NV, bool BLOCK>
+// vectors of dy, s and dsum each): adds dy s rstd to acc and stores dx.  With
+// a = dy s: dot = sum a gamma, acc += a rstd.  KEEP: g holds the thread's gamma.
+template <int NV, bool BLOCK, bool KEEP>
 __device__ __forceinline__ void bwd_row(const uint4 (&vd)[NV], const uint4 (&vs)[NV],
                                         const uint4 (&ve)[NV], float r,
-                                        const float* __restrict__ gamma, int t, int G, int nvec,
-                                        int cols, float* red, float (&acc)[NV][8], bf16* out) {
-  float dot = 0.f;
+                                        const float* __restrict__ gamma, F2 (&g)[NV][4], int t,
+                                        int G, int nvec, int cols, float* red, F2 (&acc)[NV][4],
+                                        bf16* out) {
+  F2 dot2 = f2(0.f, 0.f);
+  const F2 r2 = f2(r, r);
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int u = t + j * G;
-    float d[8], s[8], g[8] = {};
-    unpack8_bits(vd[j], d);
-    unpack8_bits(vs[j], s);
-    if (u < nvec) load8(gamma + 8 * u, g);
+    if (!KEEP) load_gamma(gamma, t + j * G, nvec, g[j]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      dot += d[i] * g[i] * s[i];
-      acc[j][i] += d[i] * (s[i] * r);
+    for (int i = 0; i < 4; ++i) {
+      const F2 a = f2_mul(f2_bf16(word(vd[j], i)), f2_bf16(word(vs[j], i)));
+      dot2 = f2_fma(a, g[j][i], dot2);
+      acc[j][i] = f2_fma(a, r2, acc[j][i]);
     }
   }
-  dot = row_sum<BLOCK>(dot, red);
-  const float c = r * r * (dot / static_cast<float>(cols));
+  const float2 dd = f2_get(dot2);
+  const float dot = row_sum<BLOCK>(dd.x + dd.y, red);
+  const float c = -r * (r * r * (dot / static_cast<float>(cols)));
+  const F2 c2 = f2(c, c);
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int u = t + j * G;
+    if (!KEEP) load_gamma(gamma, u, nvec, g[j]);
     if (u < nvec) {
-      float d[8], s[8], g[8], e[8];
-      unpack8_bits(vd[j], d);
-      unpack8_bits(vs[j], s);
-      unpack8_bits(ve[j], e);
-      load8(gamma + 8 * u, g);
+      uint32_t o[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) d[i] = r * (d[i] * g[i] - s[i] * c) + e[i];
-      *reinterpret_cast<uint4*>(out + 8 * u) = pack8(d);
+      for (int i = 0; i < 4; ++i) {
+        const F2 w = f2_mul(f2_bf16(word(vd[j], i)), g[j][i]);
+        const F2 e = f2_fma(f2_bf16(word(vs[j], i)), c2, f2_bf16(word(ve[j], i)));
+        const float2 y = f2_get(f2_fma(w, r2, e));
+        o[i] = pack_bf16(y.x, y.y);
+      }
+      *reinterpret_cast<uint4*>(out + 8 * u) = make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
 }
 template <int NV>
-__device__ __forceinline__ void put_acc(const float (&acc)[NV][8], int t, int G, int nvec,
+__device__ __forceinline__ void put_acc(const F2 (&acc)[NV][4], int t, int G, int nvec,
                                         float* p) {
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int u = t + j * G;
     if (u < nvec) {
-      *reinterpret_cast<float4*>(p + 8 * u) =
-          make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
-      *reinterpret_cast<float4*>(p + 8 * u + 4) =
-          make_float4(acc[j][4], acc[j][5], acc[j][6], acc[j][7]);
+#pragma unroll
+      for (int i = 0; i < 4; i += 2) {
+        const float2 x = f2_get(acc[j][i]), y = f2_get(acc[j][i + 1]);
+        *reinterpret_cast<float4*>(p + 8 * u + 2 * i) = make_float4(x.x, x.y, y.x, y.y);
+      }
     }
   }
 }
@@ -207,14 +251,16 @@ __device__ __forceinline__ void put_acc(const float (&acc)[NV][8], int t, int G,
 // of this block ahead.  A block walks rows blockIdx.x, blockIdx.x + gridDim.x,
 // ...; a thread's columns are the same in all of them, so the sums of dy s rstd
 // stay in registers and each block writes one row of `parts` at its end.
-// Bound by its bytes (dy, s, dsum, dx: 8 per column): 27 us at 4001 x 4112, 4.8
-// TB/s (47 us and 5.7 at 8192 x 4096), and 5 more for the sum of `parts`.
-// Loads into registers one row ahead instead took 107 registers, which leaves
-// one block of nine warps per SM (33 us); at 96 the compiler gave up the
-// look-ahead (31 us).  One vector per thread (NV = 1) instead of two halves a
-// row's way through the block: 29.4 -> 27.2 us.
+// Bound by its bytes (dy, s, dsum, dx: 8 per column): 42 us at 8192 x 4096, 6.3
+// TB/s, and 24.5 us at 4001 x 4112; the sum of `parts` takes 4 more.  On the
+// way: rows loaded into registers one ahead took 107 registers, which leaves one
+// block of nine warps per SM (4001 x 4112: 33 us; at 96 the compiler gave up
+// the look-ahead, 31 us); staged rows with two vectors per thread 29.4, with one
+// 27.2, with packed fp32 arithmetic and gamma kept in registers 24.5.
+// 56 registers: nine warps per quarter of an SM, so that two blocks of 17 warps
+// (4112 columns) are resident.
 template <int NV>
-__global__ void __launch_bounds__(NV == 1 ? 1024 : 512)
+__global__ void __maxnreg__(NV == 1 ? 56 : 128)
     k_rmsnorm_bwd_staged(const bf16* dy, const bf16* dsum, const bf16* sum,
                          const float* __restrict__ gamma, const float* __restrict__ rstd,
                          int64_t rows, int cols, bf16* dx, float* __restrict__ parts, int stages,
@@ -250,12 +296,20 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512)
     int64_t row = blockIdx.x;
     for (int i = 0; i < stages && row < rows; ++i, row += gridDim.x) fetch(row, i);
   }
-  float acc[NV][8] = {};
+  constexpr bool KEEP = NV == 1;
+  F2 acc[NV][4], g[NV][4];
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[j][i] = f2(0.f, 0.f);
   RingPos r;
   int flip = 0;
   const uint4 zero = make_uint4(0, 0, 0, 0);
+  if (KEEP) load_gamma(gamma, t, nvec, g[0]);
+  float rs_next = blockIdx.x < rows ? rstd[blockIdx.x] : 0.f;
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, r.next(stages), flip ^= 1) {
-    const float rs = rstd[row];
+    const float rs = rs_next;
+    if (row + gridDim.x < rows) rs_next = rstd[row + gridDim.x];
     // a wait that runs out leaves the rest of the call meaningless, not stuck
     mbar_wait(smem_u32(bars + r.slot), r.phase, status, abort_flag);
     const uint8_t* at = ring + r.slot * stage_bytes;
@@ -270,7 +324,8 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512)
     }
     // every thread has its part of the row before row_sum's barrier, so the
     // slot is free after it
-    bwd_row<NV, true>(vd, vs, ve, rs, gamma, t, G, nvec, cols, red[flip], acc, dx + row * cols);
+    bwd_row<NV, true, KEEP>(vd, vs, ve, rs, gamma, g, t, G, nvec, cols, red[flip], acc,
+                            dx + row * cols);
     const int64_t next = row + static_cast<int64_t>(stages) * gridDim.x;
     if (t == 0 && next < rows && !*abort_flag) fetch(next, r.slot);
   }
@@ -300,7 +355,16 @@ __global__ void __launch_bounds__(BLOCK ? 1024 : 256)
   const int64_t step = BLOCK ? gridDim.x : static_cast<int64_t>(gridDim.x) * 8;
   const int nvec = cols >> 3;
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  float acc[NV][8] = {};
+  F2 acc[NV][4], g[NV][4];
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[j][i] = f2(0.f, 0.f);
+  constexpr bool KEEP = NV <= 2;
+  if (KEEP) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) load_gamma(gamma, t + j * G, nvec, g[j]);
+  }
   int flip = 0;
   for (int64_t row = first; row < rows; row += step, flip ^= 1) {
     uint4 vd[NV], vs[NV], ve[NV];
@@ -312,8 +376,8 @@ __global__ void __launch_bounds__(BLOCK ? 1024 : 256)
       vs[j] = u < nvec ? *reinterpret_cast<const uint4*>(sum + at) : zero;
       ve[j] = u < nvec && dsum ? *reinterpret_cast<const uint4*>(dsum + at) : zero;
     }
-    bwd_row<NV, BLOCK>(vd, vs, ve, rstd[row], gamma, t, G, nvec, cols, red[flip], acc,
-                       dx + row * cols);
+    bwd_row<NV, BLOCK, KEEP>(vd, vs, ve, rstd[row], gamma, g, t, G, nvec, cols, red[flip], acc,
+                             dx + row * cols);
   }
   if (!parts) return;
   if (BLOCK) {
@@ -330,26 +394,36 @@ __global__ void __launch_bounds__(BLOCK ? 1024 : 256)
   }
 }
 
-// out[c] = sum over n rows of parts[.][c], in a fixed order: 8 columns (one
-// sector) per block, 64 groups of rows.
+// out[c] = sum over n rows of parts[.][c], in a fixed order: 4 Q columns per
+// block, Q threads of four columns each for 512 / Q groups of rows.  Q = 8 (a
+// line) for wide rows; Q = 2 (a sector) keeps the SMs busy with narrow ones,
+// which also have more rows of parts.
+template <int Q>
 __global__ void __launch_bounds__(512)
     k_sum_parts(const float* __restrict__ parts, int n, int cols, float* __restrict__ out) {
-  __shared__ float red[16][8];
+  __shared__ float4 red[16][Q];
   grid_dep_launch();
   grid_dep_wait();
-  const int c = blockIdx.x * 8 + (threadIdx.x & 7), grp = threadIdx.x >> 3;
-  float a = 0.f;
-#pragma unroll 8
-  for (int i = grp; i < n; i += 64) a += parts[static_cast<size_t>(i) * cols + c];
-  a += __shfl_xor_sync(0xFFFFFFFFu, a, 8);
-  a += __shfl_xor_sync(0xFFFFFFFFu, a, 16);
-  if ((threadIdx.x & 31) < 8) red[threadIdx.x >> 5][threadIdx.x & 7] = a;
-  __syncthreads();
-  if (threadIdx.x < 8) {
-    a = 0.f;
+  const int quad = threadIdx.x % Q, grp = threadIdx.x / Q;
+  const int c = (blockIdx.x * Q + quad) * 4;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](const float4& b) { a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w; };
+  if (c < cols) {
+#pragma unroll 5
+    for (int i = grp; i < n; i += 512 / Q)
+      add(*reinterpret_cast<const float4*>(parts + static_cast<size_t>(i) * cols + c));
+  }
 #pragma unroll
-    for (int w = 0; w < 16; ++w) a += red[w][threadIdx.x];
-    out[c] = a;
+  for (int o = Q; o <= 16; o <<= 1)
+    add(make_float4(__shfl_xor_sync(0xFFFFFFFFu, a.x, o), __shfl_xor_sync(0xFFFFFFFFu, a.y, o),
+                    __shfl_xor_sync(0xFFFFFFFFu, a.z, o), __shfl_xor_sync(0xFFFFFFFFu, a.w, o)));
+  if ((threadIdx.x & 31) < Q) red[threadIdx.x >> 5][quad] = a;
+  __syncthreads();
+  if (threadIdx.x < Q && c < cols) {
+    a = red[0][quad];
+#pragma unroll
+    for (int w = 1; w < 16; ++w) add(red[w][quad]);
+    *reinterpret_cast<float4*>(out + c) = a;
   }
 }
 
@@ -517,7 +591,10 @@ cudaError_t launch_rmsnorm_bwd(const bf16* dy, const bf16* dsum, const bf16* sum
                   8 * cols * 4, 0, s, dy, dsum, sum, gamma, rstd, rows, cols, dx, into, status);
   }
   if (dgamma && e == cudaSuccess) {
-    e = ff_launch(k_sum_parts, cols / 8, 512, 0, 0, s, parts, bs.grid, cols, dgamma);
+    e = cols >= 4096 ? ff_launch(k_sum_parts<8>, (cols + 31) / 32, 512, 0, 0, s, parts, bs.grid,
+                                 cols, dgamma)
+                     : ff_launch(k_sum_parts<2>, cols / 8, 512, 0, 0, s, parts, bs.grid, cols,
+                                 dgamma);
     count_launch();
   }
   return e;
