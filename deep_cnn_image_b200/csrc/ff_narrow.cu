@@ -418,9 +418,9 @@ bool ff_narrow_product(const FfProduct& p, cudaStream_t s, cudaError_t* err) {
 // then the slowest of reading the weights (6.3 TB/s, 5.5 with about one CTA per
 // SM, at most 45 GB/s per CTA), moving all operands into the SMs (12 TB/s), and
 // the steps of K that one SM walks (0.27 us each); a second wave of CTAs starts
-// over (4.5 us).  Over 230
-// sizes the kernel that this and ff_pair_ns choose takes 1% more than the
-// faster of the two in the mean.
+// over (4.5 us).  Over 230 sizes the kernel that this and ff_pair_ns choose takes
+// 0.1% more than the faster of the two in the mean.
+//
 // Clusters of more than four lost to four at every size measured (they leave
 // SMs of a GPC over and join more slowly), so S <= 4.  Two CTAs per SM have
 // 112 KB each: four stages up to 64 tokens but three at 128, which is too few

@@ -618,3 +618,63 @@ def test_block_captured(ax, B, In, F):
         assert all(torch.equal(b[k], other[k]) for k in RESULTS)
     torch.cuda.synchronize()
     del graph
+
+
+FIRST = """
+import sys
+import torch
+sys.path.insert(0, %r)
+from deep_cnn_image_b200 import alexnet as ax
+from tests import test_gpu_ff as t
+b, go = t._block(ax, 71, %d, 512, 1040)
+st = torch.cuda.Stream()
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph, stream=st):
+    go()
+graph.replay()
+torch.cuda.synchronize()
+got = {k: b[k].clone() for k in t.RESULTS}
+go()
+torch.cuda.synchronize()
+assert all(torch.equal(b[k], got[k]) for k in t.RESULTS)
+print("the same")
+"""
+
+
+@pytest.mark.parametrize("B", [1, 300])
+def test_first_calls_of_a_process_captured(ax, B):
+    """No call needs an eager one before its capture."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST % (root, B)], capture_output=True, text=True, timeout=300, cwd=root)
+    assert r.returncode == 0 and "the same" in r.stdout, r.stdout + r.stderr
+
+
+def test_block_from_threads(ax):
+    """Host threads call at the same time, each on its own stream and buffers."""
+    import threading
+    import torch
+    made = [_block(ax, 81 + 10 * i, B, 512, 784) for i, B in enumerate((1, 40, 300))]
+    alone = []
+    for b, go in made:
+        go()
+        torch.cuda.synchronize()
+        alone.append({k: b[k].clone() for k in RESULTS})
+    wrong = []
+
+    def work_on(i):
+        b, go = made[i]
+        st = torch.cuda.Stream()
+        for _ in range(20):
+            go(st)
+            st.synchronize()
+            if not all(torch.equal(b[k], alone[i][k]) for k in RESULTS):
+                wrong.append(i)
+
+    threads = [threading.Thread(target=work_on, args=(i,)) for i in range(len(made))]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert not wrong
