@@ -53,7 +53,7 @@ struct FfNarrowPlan {
   bool two;  // two CTAs per SM
   double ns;
 };
-FfNarrowPlan ff_narrow_plan(int tokens, int rows, int kblocks);
+FfNarrowPlan ff_narrow_plan(int tokens, int rows, int kblocks, bool tokens_fastest);
 // the expected time of the same product on pairs of CTAs
 double ff_pair_ns(int tokens, int rows, int kblocks);
 

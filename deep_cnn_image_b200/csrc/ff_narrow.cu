@@ -79,8 +79,9 @@ __device__ __forceinline__ float4 gate4(const float4& g, const float4& u, int ac
                      gate_value(g.z, act) * u.z, gate_value(g.w, act) * u.w);
 }
 
-// W_MN: the weights are stored with their rows (the M side) fastest.
-template <int F8, int W_MN, int BN, int OUT>
+// W_MN: the weights are stored with their rows (the M side) fastest; X_MN: the
+// activations with their tokens.
+template <int F8, int W_MN, int X_MN, int BN, int OUT>
 __global__ void __launch_bounds__(THREADS)
     k_narrow(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
              const __grid_constant__ CUtensorMap tmSW, const __grid_constant__ CUtensorMap tmSX,
@@ -137,7 +138,7 @@ __global__ void __launch_bounds__(THREADS)
   if (S > 1) cluster_arrive();  // this CTA runs: the others may write to it
   const int tokens = min(BN, args.tokens - tt * BN);  // of this tile
   // with `fold` two rows of the activations make one token, and stay together
-  constexpr bool FOLDS = W_MN && OUT == FF_BF16;
+  constexpr bool FOLDS = W_MN && !X_MN && OUT == FF_BF16;
   const int terms = FOLDS && args.fold ? 2 : 1;
   const int share = (BN / terms + S - 1) / S * terms;  // of them per CTA
   // where the partial sums go: S copies of [share][128], behind the barriers
@@ -182,7 +183,13 @@ __global__ void __launch_bounds__(THREADS)
           tma_load_2d(dW, &tmW, kb * 64, w0, fb);
           tma_load_2d(dW + BOX_BYTES, &tmW, kb * 64, w1, fb);
         }
-        tma_load_2d(sX + s * X_BYTES, &tmX, kb * 64, tt * BN, fb);
+        if (X_MN) {
+#pragma unroll
+          for (int j = 0; j < BN / 64; ++j)
+            tma_load_2d(sX + s * X_BYTES + j * BOX_BYTES, &tmX, tt * BN + j * 64, kb * 64, fb);
+        } else {
+          tma_load_2d(sX + s * X_BYTES, &tmX, kb * 64, tt * BN, fb);
+        }
         if (with_scales) {
           const uint32_t dS = sS + s * SCALES;
           tma_load_2d(dS, &tmSW, 0, wt * args.k_tiles + (kb >> 2), fb);
@@ -194,10 +201,11 @@ __global__ void __launch_bounds__(THREADS)
     if (lane == 0) {
       const uint64_t a0 =
           W_MN ? smem_desc_sw128(sW, BOX_BYTES, 1024) : smem_desc_sw128(sW, 16, 1024);
-      const uint64_t b0 = smem_desc_sw128(sX, 16, 1024);
+      const uint64_t b0 =
+          X_MN ? smem_desc_sw128(sX, BOX_BYTES, 1024) : smem_desc_sw128(sX, 16, 1024);
       const uint32_t a_lo = static_cast<uint32_t>(a0), a_hi = static_cast<uint32_t>(a0 >> 32);
       const uint32_t b_lo = static_cast<uint32_t>(b0), b_hi = static_cast<uint32_t>(b0 >> 32);
-      constexpr int AS = W_MN ? 128 : 2;
+      constexpr int AS = W_MN ? 128 : 2, BS = X_MN ? 128 : 2;
       RingPos r;
       uint32_t scale_buf = 0, sa = 0;
       bool ok = true;
@@ -218,7 +226,7 @@ __global__ void __launch_bounds__(THREADS)
         const uint32_t idesc = F8 ? args.idesc | idesc_f8_byte(kb & 3) : args.idesc;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const uint64_t da = desc_at(a_hi, al + k * AS), db = desc_at(b_hi, bl + k * 2);
+          const uint64_t da = desc_at(a_hi, al + k * AS), db = desc_at(b_hi, bl + k * BS);
           const uint32_t keep = (kb > kb0 || k) ? 1u : 0u;
           if (F8)
             mma_f8<0>(tmem_base, da, db, idesc, sa, sa + 4, keep);
@@ -330,17 +338,16 @@ __global__ void __launch_bounds__(THREADS)
   }
 }
 
-template <int F8, int W_MN, int BN, int OUT>
+template <int F8, int W_MN, int X_MN, int BN, int OUT>
 cudaError_t launch(const CUtensorMap (&tm)[4], const NarrowArgs& a, int stages, int S, int tiles,
                    cudaStream_t s) {
   static bool ready[64] = {};
-  if (cudaError_t e = ff_all_smem(k_narrow<F8, W_MN, BN, OUT>, ready)) return e;
+  if (cudaError_t e = ff_all_smem(k_narrow<F8, W_MN, X_MN, BN, OUT>, ready)) return e;
   count_launch();
-  return ff_launch(k_narrow<F8, W_MN, BN, OUT>, static_cast<int64_t>(tiles) * S, THREADS,
+  return ff_launch(k_narrow<F8, W_MN, X_MN, BN, OUT>, static_cast<int64_t>(tiles) * S, THREADS,
                    stages * (W_BYTES + BN * 128 + (F8 ? SCALES : 0)) + 1024 + 512 +
                        (S > 1 ? (BN + 2 * S) * 512 : 0),
-                   S, s, tm[0],
-                   tm[1], tm[2], tm[3], a, stages, S);
+                   S, s, tm[0], tm[1], tm[2], tm[3], a, stages, S);
 }
 
 }  // namespace
@@ -348,17 +355,18 @@ cudaError_t launch(const CUtensorMap (&tm)[4], const NarrowArgs& a, int stages, 
 bool ff_narrow_product(const FfProduct& p, cudaStream_t s, cudaError_t* err) {
   // here the activations are p.a [tokens, K] and the weights p.b
   const bool gated = p.out_kind == FF_GATED;
-  if (p.a_mn || (p.b_mn && (p.f8 || gated)) || p.save.q) return false;
-  if (p.fold && (!p.b_mn || p.out_kind != FF_BF16 || p.M > 128)) return false;
+  if ((p.b_mn && (p.f8 || gated)) || (p.a_mn && !p.b_mn) || p.save.q) return false;
+  if (p.fold && (!p.b_mn || p.a_mn || p.out_kind != FF_BF16 || p.M > 128)) return false;
   const int K = p.f8 ? p.K / 2 : p.K;
   const int kblocks = (K + 63) / 64;
-  const FfNarrowPlan plan = ff_narrow_plan(p.M, gated ? 2 * p.N : p.N, kblocks);
+  const FfNarrowPlan plan = ff_narrow_plan(p.M, gated ? 2 * p.N : p.N, kblocks, p.a_mn);
   const int bn = plan.bn;
   CUtensorMap tm[4];
   memset(tm, 0, sizeof(tm));
   if (!(p.b_mn ? make_tmap_bf16(&tm[0], p.b, p.N, K, 2ull * p.N, 64, 64)
                : make_tmap_bf16(&tm[0], p.b, K, gated ? 2 * p.N : p.N, 2ull * K, 64, 64)) ||
-      !make_tmap_bf16(&tm[1], p.a, K, p.M, 2ull * K, 64, bn))
+      !(p.a_mn ? make_tmap_bf16(&tm[1], p.a, p.M, K, 2ull * p.M, 64, 64)
+               : make_tmap_bf16(&tm[1], p.a, K, p.M, 2ull * K, 64, bn)))
     return false;
   NarrowArgs a;
   memset(&a, 0, sizeof(a));
@@ -381,7 +389,7 @@ bool ff_narrow_product(const FfProduct& p, cudaStream_t s, cudaError_t* err) {
       return false;
     a.idesc = idesc_f8(128, bn, p.b_e5m2, p.a_e5m2);
   } else {
-    a.idesc = idesc_bf16(128, bn, p.b_mn, 0);
+    a.idesc = idesc_bf16(128, bn, p.b_mn, p.a_mn);
   }
   a.per = (a.kblocks + plan.split - 1) / plan.split;
   const int tiles = plan.tiles, S = plan.split;
@@ -394,14 +402,15 @@ bool ff_narrow_product(const FfProduct& p, cudaStream_t s, cudaError_t* err) {
   if (stages > a.per) stages = a.per;
   // with S = 1 the accumulator's copy (512 bytes per token) takes their place
   while (S == 1 && stages * stage < bn * 512) ++stages;
-#define ALX_NARROW(F8_, MN_, OUT_, BN_)                                              \
-  if (p.f8 == F8_ && p.b_mn == MN_ && p.out_kind == OUT_ && bn == BN_) {              \
-    *err = launch<F8_, MN_, BN_, OUT_>(tm, a, stages, S, tiles, s);                   \
-    return true;                                                                      \
+#define ALX_NARROW(F8_, MN_, XMN_, OUT_, BN_)                                                  \
+  if (p.f8 == F8_ && p.b_mn == MN_ && p.a_mn == XMN_ && p.out_kind == OUT_ && bn == BN_) {      \
+    *err = launch<F8_, MN_, XMN_, BN_, OUT_>(tm, a, stages, S, tiles, s);                       \
+    return true;                                                                                \
   }
-#define ALX_NARROW_ALL(F8_, MN_, OUT_)                                                \
-  ALX_NARROW(F8_, MN_, OUT_, 16) ALX_NARROW(F8_, MN_, OUT_, 32)                       \
-  ALX_NARROW(F8_, MN_, OUT_, 64) ALX_NARROW(F8_, MN_, OUT_, 128)
+#define ALX_NARROW_ALL(F8_, MN_, OUT_)                                                          \
+  ALX_NARROW(F8_, MN_, 0, OUT_, 16) ALX_NARROW(F8_, MN_, 0, OUT_, 32)                           \
+  ALX_NARROW(F8_, MN_, 0, OUT_, 64) ALX_NARROW(F8_, MN_, 0, OUT_, 128)
+  ALX_NARROW(0, 1, 1, FF_BF16, 128)
   ALX_NARROW_ALL(0, 0, FF_GATED)
   ALX_NARROW_ALL(0, 0, FF_F32)
   ALX_NARROW_ALL(0, 1, FF_BF16)
@@ -425,9 +434,11 @@ bool ff_narrow_product(const FfProduct& p, cudaStream_t s, cudaError_t* err) {
 // SMs of a GPC over and join more slowly), so S <= 4.  Two CTAs per SM have
 // 112 KB each: four stages up to 64 tokens but three at 128, which is too few
 // to cover a load's latency, so that split is not made there.
-FfNarrowPlan ff_narrow_plan(int tokens, int rows, int kblocks) {
+FfNarrowPlan ff_narrow_plan(int tokens, int rows, int kblocks, bool tokens_fastest) {
   const double sms = ff_num_sms();
-  const int bn = tokens <= 16 ? 16 : (tokens <= 32 ? 32 : (tokens <= 64 ? 64 : 128));
+  // tokens stored fastest come in boxes of 64, and are many (weight gradients)
+  const int bn = tokens_fastest || tokens > 64 ? 128
+                                               : (tokens <= 16 ? 16 : (tokens <= 32 ? 32 : 64));
   FfNarrowPlan p;
   p.bn = bn;
   p.tiles = ((rows + 127) / 128) * ((tokens + bn - 1) / bn);

@@ -41,14 +41,13 @@ bool gated_dims(int B, int In, int F, int step) {
 // block 4096 -> 9216 with 1 token 27 / 43, 128 tokens 32 / 33, 384 tokens 73 /
 // 53; 8-bit product 9216 -> 4096 with 128 tokens 15 / 32, 512 tokens 29 / 32.
 bool runs_narrow(const FfProduct& p) {
-  if (p.a_mn) return false;
   if (p.fold) return true;
   const int rows = p.out_kind == FF_GATED ? 2 * p.N : p.N;
   const int kblocks = ((p.f8 ? p.K : 2 * p.K) + 127) / 128;
   // with 8-bit checkpoints the narrow kernel leaves gate and codes to a second
   // one (5 us at 333 tokens); the block takes one way whatever it keeps
   const double more = p.out_kind == FF_GATED && p.M > 128 ? 3000 : 0;
-  return ff_narrow_plan(p.M, rows, kblocks).ns + more < ff_pair_ns(p.M, rows, kblocks);
+  return ff_narrow_plan(p.M, rows, kblocks, p.a_mn).ns + more < ff_pair_ns(p.M, rows, kblocks);
 }
 
 alexnet_status product(const FfProduct& p, cudaStream_t s) {
