@@ -85,10 +85,11 @@ struct GateInput {
 // Up to this many tokens the backward's dz is kept in two bf16 terms, whose sum
 // is exact to 2^-16: row 2b holds the rounded values of token b, row 2b + 1 what
 // the rounding left over, and the input's rows are doubled to match.  Its
-// products are bound by the weights there, not by their rows, and with few
-// tokens dz's rounding does not average out: at 8 tokens it made dx's error 1.5
-// times that of its own last rounding.
-constexpr int TWO_TERM_TOKENS = 64;
+// products are bound by the weights there, not by their rows (dx of 9216 ->
+// 4096: 31 us with 32 tokens in two terms, 30 with 33 in one; 64 in two took 38
+// against 31), and with few tokens dz's rounding does not average out: at 8
+// tokens it made dx's error 1.5 times that of its own last rounding.
+constexpr int TWO_TERM_TOKENS = 32;
 // z fp32 [B, 2F] -> h, and z in what `save` holds
 cudaError_t launch_gate_fwd(const float* z, int B, int F, int act, bf16* h, const GateSave& save,
                             cudaStream_t s);

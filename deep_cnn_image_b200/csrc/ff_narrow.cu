@@ -53,6 +53,7 @@ struct NarrowArgs {
   int kblocks, per;        // 128-byte steps of K, and how many a CTA takes
   int token_tiles;
   int k_tiles;             // scale tiles per 128 rows
+  const uint8_t *w_scales, *x_scales;
   int act;
   int fresh, fold;
   uint32_t idesc;
@@ -84,7 +85,6 @@ __device__ __forceinline__ float4 gate4(const float4& g, const float4& u, int ac
 template <int F8, int W_MN, int X_MN, int BN, int OUT>
 __global__ void __launch_bounds__(THREADS)
     k_narrow(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
-             const __grid_constant__ CUtensorMap tmSW, const __grid_constant__ CUtensorMap tmSX,
              const __grid_constant__ NarrowArgs args, int stages, int S) {
   constexpr int X_BYTES = BN * 128;
   constexpr int STAGE_SCALES = F8 ? SCALES : 0;
@@ -147,10 +147,6 @@ __global__ void __launch_bounds__(THREADS)
   if (warp == 8 && lane == 0) {
     tma_prefetch_desc(&tmW);
     tma_prefetch_desc(&tmX);
-    if (F8) {
-      tma_prefetch_desc(&tmSW);
-      tma_prefetch_desc(&tmSX);
-    }
     // While the kernel before this one ends, the first weights come to L2.
     // That is safe even where that kernel writes them: L2 holds its writes.
     for (int kb = kb0; kb < min(kb1, kb0 + AHEAD); ++kb) {
@@ -192,8 +188,10 @@ __global__ void __launch_bounds__(THREADS)
         }
         if (with_scales) {
           const uint32_t dS = sS + s * SCALES;
-          tma_load_2d(dS, &tmSW, 0, wt * args.k_tiles + (kb >> 2), fb);
-          tma_load_2d(dS + F8_TILE_BYTES, &tmSX, 0, tt * args.k_tiles + (kb >> 2), fb);
+          const size_t kt = kb >> 2, kts = args.k_tiles;
+          bulk_load(dS, args.w_scales + (wt * kts + kt) * F8_TILE_BYTES, F8_TILE_BYTES, fb);
+          bulk_load(dS + F8_TILE_BYTES, args.x_scales + (tt * kts + kt) * F8_TILE_BYTES,
+                    F8_TILE_BYTES, fb);
         }
       }
     }
@@ -339,7 +337,7 @@ __global__ void __launch_bounds__(THREADS)
 }
 
 template <int F8, int W_MN, int X_MN, int BN, int OUT>
-cudaError_t launch(const CUtensorMap (&tm)[4], const NarrowArgs& a, int stages, int S, int tiles,
+cudaError_t launch(const CUtensorMap (&tm)[2], const NarrowArgs& a, int stages, int S, int tiles,
                    cudaStream_t s) {
   static bool ready[64] = {};
   if (cudaError_t e = ff_all_smem(k_narrow<F8, W_MN, X_MN, BN, OUT>, ready)) return e;
@@ -347,7 +345,7 @@ cudaError_t launch(const CUtensorMap (&tm)[4], const NarrowArgs& a, int stages, 
   return ff_launch(k_narrow<F8, W_MN, X_MN, BN, OUT>, static_cast<int64_t>(tiles) * S, THREADS,
                    stages * (W_BYTES + BN * 128 + (F8 ? SCALES : 0)) + 1024 + 512 +
                        (S > 1 ? (BN + 2 * S) * 512 : 0),
-                   S, s, tm[0], tm[1], tm[2], tm[3], a, stages, S);
+                   S, s, tm[0], tm[1], a, stages, S);
 }
 
 }  // namespace
@@ -361,8 +359,7 @@ bool ff_narrow_product(const FfProduct& p, cudaStream_t s, cudaError_t* err) {
   const int kblocks = (K + 63) / 64;
   const FfNarrowPlan plan = ff_narrow_plan(p.M, gated ? 2 * p.N : p.N, kblocks, p.a_mn);
   const int bn = plan.bn;
-  CUtensorMap tm[4];
-  memset(tm, 0, sizeof(tm));
+  CUtensorMap tm[2];
   if (!(p.b_mn ? make_tmap_bf16(&tm[0], p.b, p.N, K, 2ull * p.N, 64, 64)
                : make_tmap_bf16(&tm[0], p.b, K, gated ? 2 * p.N : p.N, 2ull * K, 64, 64)) ||
       !(p.a_mn ? make_tmap_bf16(&tm[1], p.a, p.M, K, 2ull * p.M, 64, 64)
@@ -382,11 +379,8 @@ bool ff_narrow_product(const FfProduct& p, cudaStream_t s, cudaError_t* err) {
   a.status = p.status;
   if (p.f8) {
     a.k_tiles = (p.K + F8_TILE_COLS - 1) / F8_TILE_COLS;
-    if (!make_tmap_u32(&tm[2], p.b_scales, 128,
-                       static_cast<uint64_t>((p.N + 127) / 128) * a.k_tiles, 128, 1) ||
-        !make_tmap_u32(&tm[3], p.a_scales, 128,
-                       static_cast<uint64_t>((p.M + 127) / 128) * a.k_tiles, 128, 1))
-      return false;
+    a.w_scales = p.b_scales;
+    a.x_scales = p.a_scales;
     a.idesc = idesc_f8(128, bn, p.b_e5m2, p.a_e5m2);
   } else {
     a.idesc = idesc_bf16(128, bn, p.b_mn, p.a_mn);

@@ -258,7 +258,7 @@ ALEXNET_API alexnet_status alexnet_op_gated_fwd(const void* x, int B, int In, co
                                                 size_t ws_bytes, void* stream);
 
 /* Its gradient: with dg = dh * u * a'(g) and du = dh * a(g), both rounded to
- * bf16 for the products (up to 64 rows to the sum of two bf16 terms),
+ * bf16 for the products (up to 32 rows to the sum of two bf16 terms),
  *   dx = dg wg + du wu;  dw = [dg du]^T x
  * dh bf16 [B, F]; gu as the forward stored it; dx (nullable) bf16 [B, In];
  * dw (nullable) bf16 [2F, In]. */

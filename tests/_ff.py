@@ -153,9 +153,9 @@ def gated_fwd(x, w, kind):
 
 def gated_bwd(dh, x, g, u, w, kind):
     """dx, dw and the bounds of their errors before the last rounding.  The
-    products take the projections' gradients rounded to bf16, or, up to 64 rows,
+    products take the projections' gradients rounded to bf16, or, up to 32 rows,
     to two bf16 terms (2^-8 of 2^-8)."""
-    unit = U_BF16 if dh.shape[0] > 64 else U_BF16 ** 2
+    unit = U_BF16 if dh.shape[0] > 32 else U_BF16 ** 2
     a, d = act(g, kind)
     dz = torch.cat([dh * u * d, dh * a], 1)
     # the product's own rounding to bf16, and the activation's evaluation:
@@ -163,6 +163,6 @@ def gated_bwd(dh, x, g, u, w, kind):
     ez = unit * dz.abs() + torch.cat([(dh * u).abs() * (1 + g.abs()), (dh * g).abs()], 1) * ACT_EPS
     za, wa, xa = dz.abs() + ez, w.abs(), x.abs()
     B, F2 = dz.shape
-    B = 2 * B if B <= 64 else B  # two terms are two products
+    B = 2 * B if B <= 32 else B  # two terms are two products
     return (dz @ w, dz.t() @ x, ez @ wa + steps(F2) * ACC * (za @ wa),
             ez.t() @ xa + steps(B) * ACC * (za.t() @ xa))
