@@ -90,9 +90,9 @@ struct GateInput {
 // against 31), and with few tokens dz's rounding does not average out: at 8
 // tokens it made dx's error 1.5 times that of its own last rounding.
 constexpr int TWO_TERM_TOKENS = 32;
-// z fp32 [B, 2F] -> h, and z in what `save` holds
-cudaError_t launch_gate_fwd(const float* z, int B, int F, int act, bf16* h, const GateSave& save,
-                            cudaStream_t s);
+// z fp32 [B, 2F] -> h, and z as two 8-bit matrices
+cudaError_t launch_gate_fwd(const float* z, int B, int F, int act, bf16* h, uint8_t* guq,
+                            uint8_t* gus, cudaStream_t s);
 // dz bf16 [B, 2F] ([2B, 2F] in two terms) from dh and the saved projections, and
 // the input's values where they are wanted; *status = 0
 cudaError_t launch_gate_bwd(const bf16* dh, const GateSave& save, const GateInput& in, int B, int F,

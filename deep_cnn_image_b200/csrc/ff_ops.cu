@@ -201,7 +201,7 @@ alexnet_status gated_fwd(const void* x, int B, int In, const void* w, int F, int
     cudaError_t e = cudaSuccess;
     if (!ff_narrow_product(both, s, &e)) return ALEXNET_ERR_UNSUPPORTED;
     if (e) return done(e);
-    return done(launch_gate_fwd(z, B, F, act, B16(h), save, s));
+    return done(launch_gate_fwd(z, B, F, act, B16(h), save.q, save.qs, s));
   }
   return product(p, s);
 }

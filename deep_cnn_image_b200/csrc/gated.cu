@@ -12,15 +12,14 @@ namespace alx {
 
 namespace {
 
-// 16 lanes per 128-column block of a row, 8 columns of g and u each: h =
-// a(g) u, and the projections themselves in bf16 or as 8-bit rows.
+// 16 lanes per 128-column block of a row, 8 columns of g and u each: h = a(g) u,
+// and the projections as 8-bit rows (after the narrow product kernel, whose
+// tiles hold half a block).
 __global__ void __launch_bounds__(256)
     k_gate_fwd(const float* __restrict__ z, int B, int F, int act, bf16* __restrict__ h,
-               const GateSave save) {
+               uint8_t* __restrict__ guq, uint8_t* __restrict__ gus) {
   grid_dep_launch();
   grid_dep_wait();
-  bf16* gu = save.b16;
-  uint8_t *guq = save.q, *gus = save.qs;
   const int blocks = (F + F8_BLOCK - 1) / F8_BLOCK;
   const int col_tiles = (F + F8_TILE_COLS - 1) / F8_TILE_COLS;
   const size_t half_s = static_cast<size_t>((B + 127) / 128) * col_tiles * F8_TILE_BYTES;
@@ -51,33 +50,21 @@ __global__ void __launch_bounds__(256)
     }
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      if (save.f32 && col < F) {
-        float4* o = reinterpret_cast<float4*>(save.f32 + row * 2 * F + k * static_cast<int64_t>(F) + col);
-        o[0] = make_float4(p[k][0], p[k][1], p[k][2], p[k][3]);
-        o[1] = make_float4(p[k][4], p[k][5], p[k][6], p[k][7]);
-      }
-      if (gu && col < F)
-        *reinterpret_cast<uint4*>(gu + row * 2 * F + k * static_cast<int64_t>(F) + col) =
-            make_uint4(pack_bf16(p[k][0], p[k][1]), pack_bf16(p[k][2], p[k][3]),
-                       pack_bf16(p[k][4], p[k][5]), pack_bf16(p[k][6], p[k][7]));
-      if (guq) {
-        float a = 0.f;
+      float a = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          p[k][i] = f8_finite(p[k][i]);
-          a = fmaxf(a, fabsf(p[k][i]));
-        }
-#pragma unroll
-        for (int o = 8; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(mask, a, o));
-        const uint32_t s = f8_scale_byte(a, 0);
-        const float inv = f8_scale_inv(s);
-        if (col < F)
-          *reinterpret_cast<uint2*>(guq + (k * static_cast<int64_t>(B) + row) * F + col) =
-              make_uint2(f8_pack4(p[k][0] * inv, p[k][1] * inv, p[k][2] * inv, p[k][3] * inv, 0),
-                         f8_pack4(p[k][4] * inv, p[k][5] * inv, p[k][6] * inv, p[k][7] * inv, 0));
-        if (sub == 0)
-          gus[k * half_s + f8_scale_at(row, blk, col_tiles)] = static_cast<uint8_t>(s);
+      for (int i = 0; i < 8; ++i) {
+        p[k][i] = f8_finite(p[k][i]);
+        a = fmaxf(a, fabsf(p[k][i]));
       }
+#pragma unroll
+      for (int o = 8; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(mask, a, o));
+      const uint32_t s = f8_scale_byte(a, 0);
+      const float inv = f8_scale_inv(s);
+      if (col < F)
+        *reinterpret_cast<uint2*>(guq + (k * static_cast<int64_t>(B) + row) * F + col) =
+            make_uint2(f8_pack4(p[k][0] * inv, p[k][1] * inv, p[k][2] * inv, p[k][3] * inv, 0),
+                       f8_pack4(p[k][4] * inv, p[k][5] * inv, p[k][6] * inv, p[k][7] * inv, 0));
+      if (sub == 0) gus[k * half_s + f8_scale_at(row, blk, col_tiles)] = static_cast<uint8_t>(s);
     }
   }
 }
@@ -207,11 +194,12 @@ int grid_for(int64_t blocks) {
 
 }  // namespace
 
-cudaError_t launch_gate_fwd(const float* z, int B, int F, int act, bf16* h, const GateSave& save,
-                            cudaStream_t s) {
+cudaError_t launch_gate_fwd(const float* z, int B, int F, int act, bf16* h, uint8_t* guq,
+                            uint8_t* gus, cudaStream_t s) {
   const int64_t blocks = static_cast<int64_t>(B) * ((F + F8_BLOCK - 1) / F8_BLOCK);
   count_launch();
-  return ff_launch(k_gate_fwd, grid_for((blocks + 15) / 16), 256, 0, 0, s, z, B, F, act, h, save);
+  return ff_launch(k_gate_fwd, grid_for((blocks + 15) / 16), 256, 0, 0, s, z, B, F, act, h, guq,
+                   gus);
 }
 
 cudaError_t launch_gate_bwd(const bf16* dh, const GateSave& save, const GateInput& in, int B, int F,
