@@ -14,16 +14,16 @@ namespace {
 
 // Sum over the threads that share a row: a warp, or (BLOCK) a whole block of
 // whole warps; the order is fixed, so results are reproducible.  `red` holds
-// 32 floats.
-template <bool BLOCK>
-__device__ __forceinline__ float row_sum(float v, float* red) {
+// 32 values.
+template <bool BLOCK, typename T>
+__device__ __forceinline__ T row_sum(T v, T* red) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   if (BLOCK) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (lane == 0) red[warp] = v;
     __syncthreads();
-    v = lane < static_cast<int>(blockDim.x >> 5) ? red[lane] : 0.f;
+    v = lane < static_cast<int>(blockDim.x >> 5) ? red[lane] : T(0);
 #pragma unroll
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   }
@@ -48,12 +48,13 @@ __device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
 }
 
 // Largest finite magnitude of f over the 16 lanes that hold a block's 128
-// values; f's infinities become NaN.
+// values; f's infinities become NaN (CLEAN; else f has none).
+template <bool CLEAN = true>
 __device__ __forceinline__ float block_amax(float (&f)[8], uint32_t mask) {
   float a = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    f[i] = f8_finite(f[i]);
+    if (CLEAN) f[i] = f8_finite(f[i]);
     a = fmaxf(a, fabsf(f[i]));
   }
 #pragma unroll
@@ -66,19 +67,58 @@ __device__ __forceinline__ uint2 codes8(const float (&f)[8], float inv, int e5m2
                     f8_pack4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv, e5m2));
 }
 
+// 1 / sqrt(m) for m > 0: the 32-bit value of m's part in [1, 4), and one
+// Newton step, which squares its error (2^-43 then).
+__device__ __forceinline__ double rsqrt64(double m) {
+  const int hi = __double2hiint(m), k = ((hi >> 20) - 1023) >> 1;
+  const double f = __hiloint2double(hi - (k << 21), __double2loint(m));
+  const double r = rsqrtf(static_cast<float>(f));
+  const double s = r * (1.5 - 0.5 * f * r * r) * __hiloint2double((1023 - k) << 20, 0);
+  return m <= 1.79e308 ? s : rsqrtf(static_cast<float>(m));  // infinity: 0, NaN: NaN
+}
+
+// How far a value lies above (a border between two codes or two scales - 3
+// units of fp32), in 2^-13 units: such a border has at most five leading bits,
+// so the low 19 of fp32's are zero there whatever its power-of-two scale.  The
+// 32-bit y is off by at most 3 units (three roundings of 2^-24 of a value under
+// 2^24 units), so further than that from all borders 32 bits decide as 64
+// would.  Zeros and infinities lie on borders too.
+constexpr uint32_t NEAR_BORDER = 6u << 13;
+__device__ __forceinline__ uint32_t over_border(float f) {
+  return __float_as_uint(f) * 8192u + (3u << 13);
+}
+__device__ __forceinline__ bool near_border(const float (&f)[8]) {
+  uint32_t m = over_border(f[0]);
+#pragma unroll
+  for (int i = 1; i < 8; ++i) m = min(m, over_border(f[i]));
+  return m <= NEAR_BORDER;
+}
+// f replaced by y cut to 32 bits with the last bit set where something was
+// cut off: such a value rounds to fewer bits as y itself does.
+__device__ __forceinline__ float round_odd(double y) {
+  const float f = __double2float_rz(y);
+  return static_cast<double>(f) == y ? f : __uint_as_float(__float_as_uint(f) | 1u);
+}
+
 // y = s * rstd * gamma with s = bf16(x + res), rstd = 1/sqrt(mean(s^2) + eps).
 // One pass over the row: G threads (a warp, eight rows per block; or BLOCK: a
 // block) hold it in registers as bf16, NV vectors of 8 columns each (thread t
 // the vectors t, t + G, ...), so the rounded s is also what the statistic and
 // the gradient see.  16 neighbouring lanes hold one 128-column block of the
-// 8-bit output.  Bound by its bytes (x, res, s, codes: 7 per column): 39 us at
-// 8192 x 4096, 6.0 TB/s, 0.91 of a copy.
+// 8-bit output.  The squares are summed in 64 bits and y next to a border
+// between two codes is computed in 64 bits again, so that a code is y rounded
+// once; in 32 bits throughout about one code in 2 million comes out as its
+// neighbour.  At 8192 x 4096 (7 bytes per column: x, res, s and the codes) that
+// is 51 us against 45, 4.6 TB/s: a block lives for 6.5 us, most of it its loads,
+// and the rest of its path is longer (summing in 32 bits, or the 64-bit part in
+// a call or after the stores, was no faster).  The bound on registers keeps
+// eight blocks of 256 on an SM (57 us with the 56 that the compiler takes).
 template <int NV, bool BLOCK>
-__global__ void __launch_bounds__(NV > 4 ? 1024 : 512)
+__global__ void __launch_bounds__(NV > 4 ? 1024 : 512, NV > 4 ? 1 : (NV > 2 ? 2 : 4))
     k_rmsnorm_fwd(const bf16* x, const bf16* res, const float* __restrict__ gamma, int64_t rows,
                   int cols, float eps, bf16* sum, bf16* y, float* rstd, uint8_t* q,
                   uint8_t* scales) {
-  __shared__ float red[32];
+  __shared__ double red[32];
   grid_dep_launch();
   grid_dep_wait();
   const int G = BLOCK ? blockDim.x : 32;
@@ -110,16 +150,17 @@ __global__ void __launch_bounds__(NV > 4 ? 1024 : 512)
       v[j] = pack8(a);
     }
   }
-  float ss = 0.f;
+  double sq[2] = {};
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     float a[8];
     unpack8_bits(v[j], a);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss += a[i] * a[i];
+    for (int i = 0; i < 8; ++i) sq[i & 1] += static_cast<double>(a[i]) * a[i];
   }
-  ss = row_sum<BLOCK>(ss, red);
-  const float r = 1.f / sqrtf(ss / static_cast<float>(cols) + eps);
+  const double ss = row_sum<BLOCK>(sq[0] + sq[1], red);
+  const double r64 = rsqrt64(ss / cols + eps);
+  const float r = static_cast<float>(r64);
   if (rstd && t == 0) rstd[row] = r;
   const int col_tiles = (cols + F8_TILE_COLS - 1) / F8_TILE_COLS;
 #pragma unroll
@@ -134,12 +175,22 @@ __global__ void __launch_bounds__(NV > 4 ? 1024 : 512)
 #pragma unroll
     for (int i = 0; i < 8; ++i) a[i] = a[i] * r * g[i];
     if (live && y) *reinterpret_cast<uint4*>(y + row * cols + 8 * u) = pack8(a);
+    if (q && near_border(a)) {
+      float b[8];
+      unpack8_bits(v[j], b);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        a[i] = f8_finite(a[i]);
+        if (over_border(a[i]) <= NEAR_BORDER && a[i] != 0.f && a[i] == a[i])
+          a[i] = round_odd(b[i] * r64 * g[i]);
+      }
+    }
     if (q) {
       if (!live) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) a[i] = 0.f;
       }
-      const uint32_t s = f8_scale_byte(block_amax(a, 0xFFFFFFFFu), 0);
+      const uint32_t s = f8_scale_byte(block_amax<false>(a, 0xFFFFFFFFu), 0);
       if (live) {
         *reinterpret_cast<uint2*>(q + row * cols + 8 * u) = codes8(a, f8_scale_inv(s), 0);
         if ((u & 15) == 0) scales[f8_scale_at(row, u >> 4, col_tiles)] = static_cast<uint8_t>(s);

@@ -213,9 +213,9 @@ ALEXNET_API alexnet_status alexnet_op_f8_dequant(const void* q, const uint8_t* s
  *   rstd = 1 / sqrt(mean(s^2) + eps);  y = s * rstd * gamma
  * x, res (nullable) bf16 [rows, cols]; gamma fp32 [cols]; sum (nullable)
  * bf16 receives s; y (nullable) bf16; rstd (nullable) fp32 [rows]; q and
- * scales (both or neither) receive y, from its fp32 values, as E4M3 8-bit
- * rows.  sum may be x or res itself.  cols % 8 == 0 (16 with q), cols <=
- * 65536 (else UNSUPPORTED); eps > 0. */
+ * scales (both or neither) receive y, rounded once, as E4M3 8-bit rows.  sum
+ * may be x or res itself.  cols % 8 == 0 (16 with q), cols <= 65536 (else
+ * UNSUPPORTED); eps > 0. */
 ALEXNET_API alexnet_status alexnet_op_rmsnorm_fwd(const void* x, const void* res,
                                                   const float* gamma, int64_t rows, int cols,
                                                   float eps, void* sum, void* y, float* rstd,

@@ -209,6 +209,67 @@ def test_norm_forward(ax, R, C, with_res):
 U32 = ff.U_F32
 
 
+@pytest.mark.parametrize("R,C", [(4096, 4096), (30000, 256), (20000, 512), (500, 16400), (100, 65536), (65536, 16)])
+def test_norm_codes_are_rounded_once(ax, R, C):
+    """Codes and scales are those of y in 64 bits, next to a border between
+    two of them as well: y comes from a sum of squares in 64 bits and a
+    reciprocal root good to 2^-42.  A border every 2^-4 of a value at the
+    closest: of 2^24 values 2^24 * 2 * 2^-42 * 2^4, one in 8000 runs, may lie
+    that near to one; in 32 bits about ten do."""
+    import torch
+    x, res, gamma = _norm_in(R, C)
+    x[R // 2] = 0
+    res[R // 2] = 0
+    s, y, y2 = out((R, C)), out((R, C)), out((R, C))
+    q, sc = out((R, C), "uint8"), out((ax.f8_scale_bytes(R, C),), "uint8")
+    ax.op_rmsnorm_fwd(x, res, gamma, R, C, EPS, s, y, None, q, sc)
+    ax.op_rmsnorm_fwd(x, res, gamma, R, C, EPS, None, y2, None, None, None)
+    eps = torch.tensor(EPS, dtype=torch.float32).item()  # as the call hands it over
+    wy, _ = ff.norm_fwd(s.double(), gamma.double(), eps)
+    wq, ws = ff.encode(wy)
+    assert torch.equal(ff.read_scales(sc, R, C), ff.read_scales(ws, R, C))
+    assert torch.equal(q, wq)
+    assert torch.equal(y, y2)  # asking for codes changes nothing else
+
+
+@pytest.mark.parametrize("C", [64, 512, 4096, 9216, 40000])
+def test_norm_range_and_values_not_finite(ax, C):
+    """Rows far outside what squares fit in 32 bits; a NaN takes its row, an
+    infinity leaves 1/inf = 0 of the others and 0 * inf of itself; a y beyond
+    32 bits (through gamma) is NaN among the codes and nothing of the rest."""
+    import torch
+    R, eps = 7, 2.0 ** -120
+    x = randn(C, R, C)
+    x[0, 3] = float("nan")
+    x[1, 5] = float("inf")
+    x[2] *= 2.0 ** 100
+    x[3] *= 2.0 ** -70
+    x[4] = 0
+    x[5, 9] = -0.0
+    x, gamma = bf16(x), f32(1 + 0.3 * randn(7, C).abs())
+    s, y, r = out((R, C)), out((R, C)), out((R,), "float32")
+    q, sc = out((R, C), "uint8"), out((ax.f8_scale_bytes(R, C),), "uint8")
+    ax.op_rmsnorm_fwd(x, None, gamma, R, C, eps, s, y, r, q, sc)
+    wy, wr = ff.norm_fwd(x.double(), gamma.double(), eps)
+    assert bool(torch.isnan(r[0])) and float(r[1]) == 0
+    within(r[1:], wr[1:], 2 * U32 * wr[1:], unit=U32)
+    lost = torch.isnan(wy)
+    assert bool(lost[0].all()) and int(lost[1].sum()) == 1 and not bool(lost[2:].any())
+    assert torch.equal(torch.isnan(y), lost) and torch.equal(torch.isnan(ff.code_values(q)), lost)
+    wq, ws = ff.encode(torch.where(lost, torch.zeros_like(wy), wy))
+    assert torch.equal(ff.read_scales(sc, R, C), ff.read_scales(ws, R, C))
+    assert torch.equal(q[~lost], wq[~lost])
+    within(y[~lost], wy[~lost], 4 * U32 * wy[~lost].abs())
+    gamma[2], gamma[C - 3] = 3e38, -3e38
+    x[6, 2], x[6, C - 3] = 300.0, 300.0
+    ax.op_rmsnorm_fwd(x, None, gamma, R, C, eps, s, y, r, q, sc)
+    wy, _ = ff.norm_fwd(x.double(), gamma.double(), eps)
+    over = torch.tensor([2, C - 3], device="cuda")
+    assert bool((wy[6, over].abs() > 3.41e38).all())
+    assert bool(torch.isinf(y[6, over]).all()) and bool(torch.isnan(ff.code_values(q)[6, over]).all())
+    assert int(torch.isnan(ff.code_values(q)[6]).sum()) == 2 and int(torch.isinf(y[6]).sum()) == 2
+
+
 def test_norm_forward_in_place(ax):
     import torch
     R, C = 19, 1536
