@@ -109,10 +109,10 @@ __device__ __forceinline__ float round_odd(double y) {
 // between two codes is computed in 64 bits again, so that a code is y rounded
 // once; in 32 bits throughout about one code in 2 million comes out as its
 // neighbour.  At 8192 x 4096 (7 bytes per column: x, res, s and the codes) that
-// is 51 us against 45, 4.6 TB/s: a block lives for 6.5 us, most of it its loads,
-// and the rest of its path is longer (summing in 32 bits, or the 64-bit part in
-// a call or after the stores, was no faster).  The bound on registers keeps
-// eight blocks of 256 on an SM (57 us with the 56 that the compiler takes).
+// is 51 us against 45, 4.6 TB/s, bound by issue slots (72% busy, 38 instructions
+// per column; summing in 32 bits, or the 64-bit part in a call or after the
+// stores, was no faster).  The bound on registers keeps eight blocks of 256 on
+// an SM (57 us with the 56 that the compiler takes; a value more to keep spills).
 template <int NV, bool BLOCK>
 __global__ void __launch_bounds__(NV > 4 ? 1024 : 512, NV > 4 ? 1 : (NV > 2 ? 2 : 4))
     k_rmsnorm_fwd(const bf16* x, const bf16* res, const float* __restrict__ gamma, int64_t rows,
